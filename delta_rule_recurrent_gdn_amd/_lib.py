@@ -31,6 +31,8 @@ GDN2_FLAG_RAW_GATES = 1
 GDN2_FLAG_SCALAR_B = 2
 GDN2_FLAG_SCALAR_W = 4
 GDN2_FLAG_SCALAR_DECAY = 8
+GDN2_FLAG_L2_NORM = 16
+GDN2_FLAG_INTERLEAVED = 32
 
 GDN2_NOALLOC_SCRATCH_BYTES = 128 * 1024 * 1024  # the device array of gdn2_fwd_chunked_noalloc
 
@@ -38,6 +40,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _U = ctypes.c_uint
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 
 # name -> (restype, argtypes), in the order of include/gdn2.h
 SIGNATURES = {
@@ -69,6 +73,20 @@ SIGNATURES = {
     "gdn2_decode_step_slots": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _U, _P]),
     "gdn2_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "gdn2_fwd_chunked_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "gdn2_linattn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "gdn2_linattn_fwd_chunked": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "gdn2_linattn_bwd_chunked": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I, _I, _F,
+                                      _I, _P]),
+    "gdn2_linattn_fwd_varlen": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "gdn2_linattn_bwd_varlen": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I,
+                                     _F, _I, _P]),
+    "gdn2_linattn_decode_step": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "gdn2_linattn_decode_step_slots": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "gdn2_qk_norm_rope_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _L, _L, _I, _I, _I, _I, _L, _L, _L, _L, _F, _F, _I,
+                                   _U, _P]),
+    "gdn2_qk_norm_rope_workspace_bytes": (_SZ, [_L, _I, _I, _I]),
+    "gdn2_qk_norm_rope_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _L, _L, _I, _I, _I, _I, _L,
+                                   _L, _L, _L, _F, _F, _I, _I, _U, _P]),
     "gdn2_status_string": (ctypes.c_char_p, [_I]),
     "gdn2_version": (_I, []),
 }

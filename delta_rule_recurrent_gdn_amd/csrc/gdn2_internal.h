@@ -270,4 +270,7 @@ bool grad_supported(int Dk, int chunk, bool f32_inputs);
 // Shapes with a compiled kernel (checked by the C ABI before launching).
 bool fwd_supported(int Dk, int Dv, int chunk, bool f32_inputs);
 
+// dst[i] = src ? src[i] : 0 for n floats (gdn2_api.hip)
+hipError_t launch_copy_or_zero(float* dst, const float* src, int64_t n, hipStream_t s);
+
 }  // namespace gdn2

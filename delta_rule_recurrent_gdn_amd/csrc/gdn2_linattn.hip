@@ -1,0 +1,145 @@
+// gdn2_linattn.hip -- linear attention with a decay for each head: launchers of the sweeps, the join of the piece
+// states, the sum over shared heads.
+//
+// A sequence of few (sequence, head) pairs leaves most of the GPU idle when one workgroup walks it whole, so it is cut
+// into pieces: a first pass sums every piece's own contribution to the state (it reads y and z alone), the join kernel
+// runs Z_in[s+1] = g^L Z_in[s] + U[s] over the pieces of a sequence, element by element, and the sweep then walks all
+// pieces at once. The price is a second read of y and z.
+
+#include "gdn2_linattn.h"
+
+#include "gdn2_common.h"
+
+namespace gdn2 {
+
+// by operand type, one translation unit each
+hipError_t launch_linattn_bf16(const LinArgs& a, bool state, hipStream_t s);
+hipError_t launch_linattn_f32(const LinArgs& a, bool state, hipStream_t s);
+
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+// One thread an element quadruple of a (sequence, head)'s state.
+__global__ __launch_bounds__(kJoinThreads) void gdn2_linattn_join_kernel(LinArgs a, int blocks) {
+  const int chain = blockIdx.x / blocks;
+  const int n = chain / a.H, h = chain - n * a.H;
+  const int at = ((blockIdx.x % blocks) * kJoinThreads + threadIdx.x) * 4;
+  if (at >= a.A * a.E) return;
+  const int row = at / a.E, col = at % a.E;
+  int nseg, slot, step;
+  if (a.cu) {
+    slot = a.seg_first[n];
+    nseg = a.seg_first[n + 1] - slot;
+    step = 1;
+  } else {
+    slot = n;
+    nseg = a.max_segs;
+    step = a.N;
+  }
+  const int64_t state = (int64_t)a.A * a.E;
+  float z[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.sw.Z0) {
+    const float* src = a.sw.Z0 + (int64_t)chain * state;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = src[(int64_t)row * a.sw.z0_rs + (int64_t)(col + e) * a.sw.z0_cs];
+  }
+  if (nseg == 0) {  // a sequence without tokens: its last state is its first
+    if (a.sw.Z1) *reinterpret_cast<float4*>(a.sw.Z1 + (int64_t)chain * state + at) = make_float4(z[0], z[1], z[2], z[3]);
+    return;
+  }
+  if (!a.pieces) return;
+  const float ld = a.log_decay[h];
+  const double d = exp((ld < -1e4f ? -1e4 : (double)ld) * a.seg_tok);
+  const float hi = (float)d, lo = (float)(d - hi);
+  float4* p = reinterpret_cast<float4*>(a.seg_state + ((int64_t)slot * a.H + h) * state + at);
+  const int64_t stride = (int64_t)step * a.H * state / 4;
+  p[0] = make_float4(z[0], z[1], z[2], z[3]);
+  float4 next = nseg > 1 ? p[stride] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 1; s < nseg; ++s) {
+    const float4 u = next;
+    if (s + 1 < nseg) next = p[(s + 1) * stride];
+    const float add[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = fmaf(z[e], hi, fmaf(z[e], lo, add[e]));
+    p[s * stride] = make_float4(z[0], z[1], z[2], z[3]);
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void gdn2_linattn_group_sum_kernel(const float* src, void* dst, int64_t n4, int heads,
+                                                                      int G, int D, const int64_t* cu, int N) {
+  // packed: the rows of the sequences alone
+  const int64_t row_size = (int64_t)heads * D;
+  const int64_t lo = cu ? cu[0] * row_size : 0, hi = cu ? cu[N] * row_size : n4 * 4;
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n4; id += (int64_t)gridDim.x * 256) {
+    const int64_t at = id * 4;                      // element of [rows, heads, D]
+    if (at < lo || at >= hi) continue;
+    const int64_t rh = at / D;
+    const int d = (int)(at - rh * D);
+    const float* p = src + rh * G * D + d;
+    float4 s = *reinterpret_cast<const float4*>(p);
+    for (int i = 1; i < G; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)i * D);
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    if constexpr (F32) st4(static_cast<float*>(dst) + at, s.x, s.y, s.z, s.w);
+    else st4(static_cast<__bf16*>(dst) + at, s.x, s.y, s.z, s.w);
+  }
+}
+
+}  // namespace
+
+int linattn_seg_tokens(int N, int T, int H, int A, int E, bool packed) {
+  (void)A;
+  constexpr int kChunk = 64, kLeast = 8, kWorkgroups = 512;
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  const int64_t wide = (int64_t)H * ((E + 63) / 64);  // workgroups a piece
+  int64_t L;
+  if (packed) {
+    L = (chunks * wide + kWorkgroups - 1) / kWorkgroups;
+  } else {
+    const int64_t pieces = N * wide >= 256 ? 1 : (kWorkgroups + N * wide - 1) / (N * wide);
+    L = (chunks + pieces - 1) / pieces;
+  }
+  if (L < kLeast) L = kLeast;
+  if (L > chunks) L = chunks;
+  return (int)(L * kChunk);
+}
+
+int linattn_max_segs(int N, int T, int seg_tok, bool packed) {
+  return packed ? T / seg_tok + N : (T + seg_tok - 1) / seg_tok;
+}
+
+hipError_t launch_linattn_sweep(const LinArgs& a, hipStream_t s) {
+  const auto run = a.f32 ? launch_linattn_f32 : launch_linattn_bf16;
+  if (a.pieces) {
+    const hipError_t e = run(a, true, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.pieces || (a.cu && a.sw.Z1)) {
+    const int blocks = (a.A * a.E / 4 + kJoinThreads - 1) / kJoinThreads;
+    hipLaunchKernelGGL(gdn2_linattn_join_kernel, dim3((unsigned)(a.N * a.H * blocks)), dim3(kJoinThreads), 0, s, a,
+                       blocks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return run(a, false, s);
+}
+
+hipError_t launch_linattn_group_sum(const float* src, void* dst, int64_t rows, int heads, int G, int D, bool f32,
+                                    const int64_t* cu, int N, hipStream_t s) {
+  const int64_t n4 = rows * heads * D / 4;
+  if (n4 == 0) return hipSuccess;
+  int64_t blocks = (n4 + 255) / 256;
+  if (blocks > 8192) blocks = 8192;
+  if (f32)
+    hipLaunchKernelGGL((gdn2_linattn_group_sum_kernel<true>), dim3((unsigned)blocks), dim3(256), 0, s, src, dst, n4,
+                       heads, G, D, cu, N);
+  else
+    hipLaunchKernelGGL((gdn2_linattn_group_sum_kernel<false>), dim3((unsigned)blocks), dim3(256), 0, s, src, dst, n4,
+                       heads, G, D, cu, N);
+  return hipGetLastError();
+}
+
+}  // namespace gdn2

@@ -1,0 +1,623 @@
+// gdn2_linattn_impl.h -- the sweep kernels of the linear attention with a decay for each head.
+//
+// The recurrence, per (sequence, head), with g = exp(log_decay) and Z an A x E matrix:
+//     Z_t = g Z_{t-1} + y_t z_t^T          r_t = Z_t^T x_t
+// Over a chunk of C tokens that Z enters (i, j count its tokens, f = `first`):
+//     r_i = sum_{j<=i} g^(i-j) (x_i . y_j) z_j + g^(i+f) Z^T x_i
+//     Z  <- g^n Z + sum_j g^(n-f-j) y_j z_j^T                          (n valid tokens, n = C but for a last chunk)
+// f = 1 is the forward recurrence; f = 0 is the reversed one of the backward, whose state holds g times the
+// gradient of the state (so the gradient of the last state enters as it is). Every power of g has an exponent
+// >= 0, so nothing overflows for g <= 1 whatever the decay, and no quotient of decays is formed.
+//
+// Work: one workgroup per (sequence, head, piece, column group of E); each wave owns 16 NT columns of the state in
+// fp32 accumulators and walks its piece chunk by chunk. Per chunk: x, y, z go to LDS (the next chunk's are in
+// flight in registers meanwhile), the waves share the C x C scores (one 16-token strip each), and every wave forms
+// its columns of r = scores z + decayed x Z and of the state update.
+//
+// Operands. A 16x16 accumulator tile holds rows 4g+r of column l%16 (g = l/16), and either operand of a product
+// takes 8 contraction indices (16 bit; fp32: 4) of row or column l%16 from a lane. State tiles 2u, 2u+1 hold the
+// state rows 32u + 8g + r and 32u + 8g + 4 + r (fp32: tile u rows 16u + 4g + r), which is the contraction order
+// that x is read in from LDS with one 16-byte access, so the state enters its product from the registers it is
+// kept in. The contraction over tokens reads y and z column-wise with the transposing LDS read (16 bit).
+//
+// Precision (16-bit inputs): products of two inputs are exact in the matrix cores' fp32 sums. The decayed z is
+// split into three bf16 terms, the state as an operand and the scores into two, so that r is rounded once, at the
+// end, and the states are fp32 sums of unrounded products.
+#pragma once
+
+#include <type_traits>
+
+#include "gdn2_common.h"
+#include "gdn2_linattn.h"
+
+namespace gdn2 {
+
+// 2^(l2 n) with the exponent reduced in fp64: one fp32 rounding for any n (n >= 0)
+__device__ __forceinline__ float decay_pow(double l2, int n) {
+  const double e = l2 * n, r = rint(e);
+  return ldexpf(__builtin_amdgcn_exp2f((float)(e - r)), (int)fmax(r, -4096.0));
+}
+
+// log2 of the decay; -1e4 stands for anything smaller (its powers are zero in fp32 from the first on), so that
+// exponent 0 gives 1 for a decay of zero too. NaN stays.
+__device__ __forceinline__ double decay_log2(float l) {
+  const double x = l < -1e4f ? -1e4 : (double)l;
+  return x * 1.4426950408889634074;
+}
+
+// Matrix operand types. unit: the contraction indices of one operand register group.
+template <bool F32>
+struct LinOp {
+  using T = typename std::conditional<F32, float, __bf16>::type;
+  using V = typename std::conditional<F32, f32x4, bf16x8>::type;
+  static constexpr int KU = F32 ? 16 : 32;
+  static constexpr int C = F32 ? 32 : 64;       // tokens a chunk
+  static constexpr int ES = F32 ? 4 : 2;        // bytes an element
+};
+
+__device__ __forceinline__ void lin_mma(f32x4& acc, const bf16x8& a, const bf16x8& b) { acc = mfma16x16x32(a, b, acc); }
+__device__ __forceinline__ void lin_mma(f32x4& acc, const f32x4& a, const f32x4& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc = mfma16x16x4(a[i], b[i], acc);
+}
+
+// A tile [rows][W] of the inputs' type in LDS, 16-byte blocks permuted within a row so that neither a wave's
+// 16-byte reads down a column of blocks nor its transposing (fp32: 4-byte) reads across rows meet in a bank.
+template <bool F32, int W>
+struct LinTile {
+  using Op = LinOp<F32>;
+  static constexpr int kRow = W * Op::ES;       // bytes a row
+  static constexpr int NB = kRow / 16;          // blocks a row
+  __device__ __forceinline__ static int perm(int r) {
+    if constexpr (NB >= 16) return F32 ? (r & 15) : (((r & 3) << 2) | ((r >> 2) & 3));
+    else if constexpr (NB == 8) return F32 ? ((r >> 1) & 7) : ((((r >> 1) & 1) << 2) | ((r >> 2) & 3));
+    else if constexpr (NB == 4) return (r >> 2) & 3;
+    else return 0;
+  }
+  // byte offset of block b of row r
+  __device__ __forceinline__ static int at(int r, int b) { return r * kRow + ((b ^ perm(r)) << 4); }
+  // operand of unit u from row r (contraction along the row), lane group g
+  __device__ __forceinline__ static typename Op::V row(const char* t, int r, int u, int g) {
+    return *reinterpret_cast<const typename Op::V*>(t + at(r, 4 * u + g));
+  }
+  // operand whose contraction runs down the rows 16-bit: 32u + 8g .. + 7, fp32: 16u + 4g .. + 3; its 16 columns are
+  // for lane l%16 = 4p + e: 16 bit: block b0 + p * bs, elements h..h+3 (four columns a 16-byte block's half), fp32:
+  // column 4 b0 + l%16
+  __device__ __forceinline__ static typename Op::V col(const char* t, int u, int g, int i, int b0, int bs, int h) {
+    if constexpr (F32) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = *reinterpret_cast<const float*>(t + at(16 * u + 4 * g + e, b0 + (i >> 2)) + 4 * (i & 3));
+      return v;
+    } else {
+      // the read takes, for every 16 lanes, 4 rows x 16 columns, lane 4 e + p giving the address of row e, columns
+      // 4p..4p+3, and hands lane i column i of the four rows
+      const int r = 32 * u + 8 * g + (i >> 2);
+      const int p = i & 3;
+      const int b = bs ? b0 + p * bs : b0 + (p >> 1);
+      const int off = bs ? 8 * h : 8 * (p & 1);
+      typedef __attribute__((address_space(3))) bf16x4 lds4;
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r, b) + off));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r + 4, b) + off));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// A chunk's rows of one tensor on their way from HBM to LDS: 16 bytes a thread and pass.
+template <bool F32, int W, int WP, int NTH>
+struct LinFetch {
+  using Op = LinOp<F32>;
+  using Tile = LinTile<F32, WP>;
+  static constexpr int NB = W * Op::ES / 16;              // blocks a row in memory
+  static constexpr int TOTAL = NB * Op::C;
+  static constexpr int NP = (TOTAL + NTH - 1) / NTH;
+  uint4 v[NP];
+  // head: this head's first element of token 0; rows pos0.. of the sequence, clamped to its last token
+  __device__ __forceinline__ void load(const char* head, int64_t row_bytes, int64_t tok0, int dir, int pos0, int len) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int id = threadIdx.x + p * NTH;
+      const int pos = min(pos0 + id / NB, len - 1);
+      v[p] = *reinterpret_cast<const uint4*>(head + (tok0 + (int64_t)dir * pos) * row_bytes + (id % NB) * 16);
+    }
+  }
+  // rows past `valid` are zeros
+  __device__ __forceinline__ void store(char* tile, int valid) const {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int id = threadIdx.x + p * NTH;
+      const int row = id / NB;
+      if (TOTAL % NTH != 0 && row >= Op::C) break;
+      const bool ok = row < valid;
+      const uint4 z = make_uint4(ok ? v[p].x : 0u, ok ? v[p].y : 0u, ok ? v[p].z : 0u, ok ? v[p].w : 0u);
+      *reinterpret_cast<uint4*>(tile + Tile::at(row, id % NB)) = z;
+    }
+  }
+};
+
+__device__ __forceinline__ bf16x8 pack_hi(const float (&x)[8]) {  // the upper halves: bf16 by truncation
+  u32x4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = __builtin_amdgcn_perm(__float_as_uint(x[2 * j + 1]), __float_as_uint(x[2 * j]), 0x07060302u);
+  return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ void sub_hi(float (&x)[8]) {           // what truncation left
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] -= __uint_as_float(__float_as_uint(x[j]) & 0xffff0000u);
+}
+__device__ __forceinline__ bf16x8 pack_rne(const float (&x)[8]) {
+  bf16x8 b;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = f32_to_bf16(x[j]);
+  return b;
+}
+
+// any element is an infinity or NaN
+__device__ __forceinline__ bool lin_non_finite(const bf16x8& x) {
+  const u32x4 w = __builtin_bit_cast(u32x4, x);
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f800000u) == 0x7f800000u || (w[j] & 0x7f80u) == 0x7f80u;
+  return odd;
+}
+__device__ __forceinline__ bool lin_non_finite(const f32x4& x) {
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) odd |= (__float_as_uint(x[j]) & 0x7f800000u) == 0x7f800000u;
+  return odd;
+}
+// infinities and NaN replaced by zeros
+__device__ __forceinline__ void lin_finite(bf16x8& x) {
+  u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if ((w[j] & 0x7f800000u) == 0x7f800000u) w[j] &= 0xffffu;
+    if ((w[j] & 0x7f80u) == 0x7f80u) w[j] &= 0xffff0000u;
+  }
+  x = __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ void lin_finite(f32x4& x) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if ((__float_as_uint(x[j]) & 0x7f800000u) == 0x7f800000u) x[j] = 0.f;
+}
+
+template <int A, int NW, int NT, bool F32>
+struct LinShape {
+  using Op = LinOp<F32>;
+  static constexpr int AP = A < Op::KU ? Op::KU : A;  // channels of x, y in LDS (16-bit: at least one unit)
+  static constexpr int CW = 16 * NT * NW;             // columns a workgroup
+  static constexpr int kXY = Op::C * AP * Op::ES;
+  static constexpr int kZ = Op::C * CW * Op::ES;
+  static constexpr int kP = Op::C * Op::C * Op::ES;
+  static constexpr int kLds = 2 * kXY + kZ + (F32 ? 1 : 2) * kP;
+  static constexpr int kLdsState = kXY + kZ;
+};
+
+// What a workgroup has to do. Returns false where there is nothing.
+struct LinTask {
+  int n, h, seg, nseg, slot;
+  int64_t tok0;    // row of the walk's first token
+  int len, pos0, pos1;
+};
+
+__device__ __forceinline__ bool lin_task(const LinArgs& a, int item, LinTask& t) {
+  // items: head fastest, then sequence (dense), then piece
+  t.h = item % a.H;
+  int rest = item / a.H;
+  int64_t begin;
+  if (a.cu) {
+    if (rest >= a.max_segs) return false;
+    t.slot = rest;
+    t.n = a.seg_seq[rest];
+    if (t.n < 0) return false;
+    t.seg = rest - a.seg_first[t.n];
+    t.nseg = a.seg_first[t.n + 1] - a.seg_first[t.n];
+    begin = a.cu[t.n];
+    t.len = (int)(a.cu[t.n + 1] - begin);
+  } else {
+    if (rest >= a.max_segs * a.N) return false;
+    t.n = rest % a.N;
+    t.seg = rest / a.N;
+    t.slot = t.seg * a.N + t.n;
+    t.nseg = a.max_segs;
+    begin = (int64_t)t.n * a.T;
+    t.len = a.T;
+  }
+  t.tok0 = a.sw.rev ? begin + t.len - 1 : begin;
+  t.pos0 = t.seg * a.seg_tok;
+  t.pos1 = min(t.len, t.pos0 + a.seg_tok);
+  return true;
+}
+
+// Block -> (item, column group): a head's column groups take workgroups 8 apart, so that they run on one XCD and
+// read x and y through its L2 once.
+__device__ __forceinline__ void lin_block(int ncg, int& item, int& cg) {
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  item = (slot / ncg) * 8 + xcd;
+  cg = slot % ncg;
+}
+
+// State row of accumulator tile m, lane group g, element r.
+template <bool F32>
+__device__ __forceinline__ int lin_state_row(int m, int g, int r) {
+  return F32 ? 16 * m + 4 * g + r : 32 * (m >> 1) + 8 * g + 4 * (m & 1) + r;
+}
+
+// the token sum of the state update: Z += sum_j y_j (c_j z_j)^T over the chunk in LDS
+template <int A, int NW, int NT, bool F32, int RT>
+__device__ __forceinline__ void lin_update(f32x4 (&Z)[RT][NT], const char* ty, const typename LinOp<F32>::V (&zv)[LinOp<F32>::C / LinOp<F32>::KU][NT],
+                                           const float (&cz)[LinOp<F32>::C / LinOp<F32>::KU][F32 ? 4 : 8], int g, int i) {
+  using Op = LinOp<F32>;
+  using TY = LinTile<F32, LinShape<A, NW, NT, F32>::AP>;
+  constexpr int UC = Op::C / Op::KU;
+#pragma unroll
+  for (int u = 0; u < UC; ++u) {
+    if constexpr (F32) {
+      f32x4 zc[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zc[n][e] = cz[u][e] * zv[u][n][e];
+#pragma unroll
+      for (int m = 0; m < RT; ++m) {
+        const f32x4 y = TY::col(ty, u, g, i, 4 * m, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) lin_mma(Z[m][n], y, zc[n]);
+      }
+    } else {
+      bf16x8 z1[NT], z2[NT], z3[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
+        z1[n] = pack_hi(x);
+        sub_hi(x);
+        z2[n] = pack_hi(x);
+        sub_hi(x);
+        z3[n] = pack_hi(x);
+      }
+#pragma unroll
+      for (int m = 0; m < RT; ++m) {
+        const bf16x8 y = TY::col(ty, u, g, i, 4 * (m >> 1), 1, m & 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          lin_mma(Z[m][n], y, z3[n]);
+          lin_mma(Z[m][n], y, z2[n]);
+          lin_mma(Z[m][n], y, z1[n]);
+        }
+      }
+    }
+  }
+}
+
+// STATE: the sum of one piece alone, from a zero state (x, r unused), stored as the entering state of the next
+// piece for the join kernel. Otherwise the sweep of one piece.
+template <int A, int NW, int NT, bool F32, bool STATE>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(LinArgs a) {
+  using Sh = LinShape<A, NW, NT, F32>;
+  using Op = LinOp<F32>;
+  using V = typename Op::V;
+  constexpr int C = Op::C, KU = Op::KU, ES = Op::ES, AP = Sh::AP, CW = Sh::CW, NTH = 64 * NW;
+  constexpr int RT = AP / 16, UK = AP / KU, UC = C / KU, TT = C / 16, EZ = F32 ? 4 : 8;
+  using TX = LinTile<F32, AP>;
+  using TZ = LinTile<F32, CW>;
+  using TP = LinTile<F32, C>;
+
+  extern __shared__ char lds[];
+  char* const ty = lds;
+  char* const tz = lds + Sh::kXY;
+  char* const tx = tz + Sh::kZ;
+  char* const tp = tx + Sh::kXY;  // scores, then (16 bit) what their first bf16 term leaves
+
+  const int ncg = (a.E + CW - 1) / CW;
+  int item, cg;
+  lin_block(ncg, item, cg);
+  LinTask t;
+  if (!lin_task(a, item, t)) return;
+  if (STATE && t.seg + 1 >= t.nseg) return;
+
+  const int l = lane_id(), g = l >> 4, i = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(wave_id());
+  const int e0 = cg * CW + w * 16 * NT;  // this wave's first column
+  const LinSweep& sw = a.sw;
+  const int dir = sw.rev ? -1 : 1;
+  const int E = a.E;
+
+  // heads of the tensors
+  const int hx = t.h / sw.xdiv, hy = t.h / sw.ydiv, hz = t.h / sw.zdiv;
+  const int64_t rbx = (int64_t)(a.H / sw.xdiv) * A * ES, rby = (int64_t)(a.H / sw.ydiv) * A * ES;
+  const int64_t rbz = (int64_t)(a.H / sw.zdiv) * E * ES;
+  const char* const px = static_cast<const char*>(sw.x) + (int64_t)hx * A * ES;
+  const char* const py = static_cast<const char*>(sw.y) + (int64_t)hy * A * ES;
+  const char* const pz = static_cast<const char*>(sw.z) + ((int64_t)hz * E + cg * CW) * ES;
+
+  LinFetch<F32, A, AP, NTH> fx, fy;
+  LinFetch<F32, CW, CW, NTH> fz;
+  if constexpr (!STATE) fx.load(px, rbx, t.tok0, dir, t.pos0, t.len);
+  fy.load(py, rby, t.tok0, dir, t.pos0, t.len);
+  fz.load(pz, rbz, t.tok0, dir, t.pos0, t.len);
+
+  // powers of the decay that a lane needs, the same in every chunk
+  const double l2 = decay_log2(a.log_decay[t.h]);
+  float cz[UC][EZ];  // of the update: token KU u + EZ g + e
+  auto set_cz = [&](int n) {
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int e = 0; e < EZ; ++e) cz[u][e] = sw.si * decay_pow(l2, max(0, n - sw.first - (KU * u + EZ * g + e)));
+  };
+  set_cz(C);
+  auto chunk_decay = [&](int n, float& hi, float& lo) {  // g^n as a sum of two floats: it multiplies the state again and again
+    const double x = exp2(l2 * n);
+    hi = (float)x;
+    lo = (float)(x - hi);
+  };
+  float gC, gClo;
+  chunk_decay(C, gC, gClo);
+  float pd[4], pm[4], g16 = 1.f, ro[TT];
+  if constexpr (!STATE) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {  // scores: token i of its tile against token 4g + r of the same tile, of the one before
+      const int d = i - 4 * g - r;
+      pd[r] = d >= 0 ? sw.si * sw.so * decay_pow(l2, d) : 0.f;
+      pm[r] = sw.si * sw.so * decay_pow(l2, 16 + d);
+    }
+    g16 = decay_pow(l2, 16);
+#pragma unroll
+    for (int k = 0; k < TT; ++k) ro[k] = sw.so * decay_pow(l2, 16 * k + i + sw.first);
+  }
+
+  // the entering state
+  f32x4 Z[RT][NT];
+#pragma unroll
+  for (int m = 0; m < RT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) Z[m][n] = zero4();
+  if constexpr (!STATE) {
+    const float* src = nullptr;
+    int rs = E, cs = 1;
+    if (a.pieces) {
+      src = a.seg_state + ((int64_t)t.slot * a.H + t.h) * A * E;
+    } else if (sw.Z0) {
+      src = sw.Z0 + ((int64_t)t.n * a.H + t.h) * A * E;
+      rs = sw.z0_rs;
+      cs = sw.z0_cs;
+    }
+    if (src) {
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = lin_state_row<F32>(m, g, r);
+            if (A >= KU || row < A) Z[m][n][r] = src[(int64_t)row * rs + (int64_t)(e0 + 16 * n + i) * cs];
+          }
+    }
+  }
+  if constexpr (A < AP) {  // the channels that pad x and y to a unit stay zero
+    for (int id = threadIdx.x; id < C * 2; id += NTH) {
+      const int row = id >> 1, b = 2 + (id & 1);
+      *reinterpret_cast<uint4*>(ty + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
+      if constexpr (!STATE) *reinterpret_cast<uint4*>(tx + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
+    }
+  }
+
+  const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
+  for (int pos = t.pos0; pos < t.pos1; pos += C) {
+    const int valid = min(C, t.pos1 - pos);
+    const bool last = pos + C >= t.pos1;
+    if constexpr (!STATE) fx.store(tx, valid);
+    fy.store(ty, valid);
+    fz.store(tz, valid);
+    __syncthreads();
+    if (!last) {
+      if constexpr (!STATE) fx.load(px, rbx, t.tok0, dir, pos + C, t.len);
+      fy.load(py, rby, t.tok0, dir, pos + C, t.len);
+      fz.load(pz, rbz, t.tok0, dir, pos + C, t.len);
+    }
+
+    f32x4 R[TT][NT];
+    if constexpr (!STATE) {
+      // scores, transposed: tile (jt, ts) holds tokens j = 16 jt + 4g + r of columns i = 16 ts + l%16
+#pragma unroll
+      for (int s = 0; s < TT / NW + (TT % NW != 0); ++s) {
+        const int ts = w + s * NW;
+        if (TT % NW != 0 && ts >= TT) break;
+        V xv[UK];
+#pragma unroll
+        for (int u = 0; u < UK; ++u) xv[u] = TX::row(tx, 16 * ts + i, u, g);
+        float far = 1.f;
+        for (int jt = ts; jt >= 0; --jt) {
+          f32x4 p = zero4();
+#pragma unroll
+          for (int u = 0; u < UK; ++u) lin_mma(p, TX::row(ty, 16 * jt + i, u, g), xv[u]);
+          if (jt == ts) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[r] = i >= 4 * g + r ? p[r] * pd[r] : 0.f;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[r] *= pm[r] * far;
+            far *= g16;
+          }
+          if constexpr (F32) {
+            *reinterpret_cast<f32x4*>(tp + TP::at(16 * ts + i, 4 * jt + g)) = p;
+          } else {
+            bf16x4 hi, lo;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              hi[r] = f32_to_bf16(p[r]);
+              lo[r] = f32_to_bf16(p[r] - bf16_to_f32(hi[r]));
+            }
+            const int at = TP::at(16 * ts + i, 2 * jt + (g >> 1)) + 8 * (g & 1);
+            *reinterpret_cast<bf16x4*>(tp + at) = hi;
+            *reinterpret_cast<bf16x4*>(tp + Sh::kP + at) = lo;
+          }
+        }
+        if constexpr (!F32) {  // a unit of 32 tokens: the tile past the diagonal of an even strip
+          if ((ts & 1) == 0) {
+            const int at = TP::at(16 * ts + i, 2 * (ts + 1) + (g >> 1)) + 8 * (g & 1);
+            *reinterpret_cast<uint2*>(tp + at) = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(tp + Sh::kP + at) = make_uint2(0u, 0u);
+          }
+        }
+      }
+      // r^T from the state: rows are columns of the state, columns are tokens
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) R[k][n] = zero4();
+#pragma unroll
+      for (int u = 0; u < UK; ++u) {
+        V zh[NT];
+        V zl[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (F32) {
+            zh[n] = Z[u][n];
+          } else {
+            float x[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][n][r], x[4 + r] = Z[2 * u + 1][n][r];
+            zh[n] = pack_hi(x);
+            sub_hi(x);
+            zl[n] = pack_rne(x);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < TT; ++k) {
+          const V xv = TX::row(tx, 16 * k + i, u, g);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (!F32) lin_mma(R[k][n], zl[n], xv);
+            lin_mma(R[k][n], zh[n], xv);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) R[k][n][r] *= ro[k];
+      __syncthreads();
+    }
+
+    // this wave's columns of z, contraction over tokens
+    V zv[UC][NT];
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        zv[u][n] = F32 ? TZ::col(tz, u, g, i, 4 * (w * NT + n), 0, 0) : TZ::col(tz, u, g, i, 2 * (w * NT + n), 0, 0);
+
+    if constexpr (!STATE) {
+      // a zero score times an infinity or NaN of a later token is NaN: such values of z are taken out of the product,
+      // and added to their own and later tokens one by one
+      V zp[UC][NT];
+      bool odd = false;
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          zp[u][n] = zv[u][n];
+          odd |= lin_non_finite(zv[u][n]);
+        }
+      const bool any_odd = __any(odd);
+      if (any_odd) {
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) lin_finite(zp[u][n]);
+      }
+#pragma unroll
+      for (int k = 0; k < TT; ++k) {
+#pragma unroll
+        for (int u = 0; u <= (16 * k) / KU; ++u) {
+          const V p = TP::row(tp, 16 * k + i, u, g);
+          if constexpr (!F32) {
+            const V pl = TP::row(tp + Sh::kP, 16 * k + i, u, g);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zp[u][n], pl);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zp[u][n], p);
+        }
+      }
+      if (any_odd) {
+#pragma unroll
+        for (int k = 0; k < TT; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll 1
+            for (int j = 0; j < 16 * (k + 1); ++j) {
+              float p;
+              if constexpr (F32) {
+                p = *reinterpret_cast<const float*>(tp + TP::at(16 * k + i, j >> 2) + 4 * (j & 3));
+              } else {
+                const char* at = tp + TP::at(16 * k + i, j >> 3) + 2 * (j & 7);
+                p = bf16_to_f32(*reinterpret_cast<const __bf16*>(at)) +
+                    bf16_to_f32(*reinterpret_cast<const __bf16*>(at + Sh::kP));
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int c = 16 * (w * NT + n) + 4 * g + r;
+                const float z = load1<F32>(tz + TZ::at(j, c * ES / 16), c % (16 / ES));
+                if (j <= 16 * k + i && !(fabsf(z) <= 3.4028235e38f)) R[k][n][r] += p * z;
+              }
+            }
+      }
+      // store: a lane has 4 neighbouring columns of token 16 k + i
+      const int64_t rrow = (int64_t)a.H * E;
+#pragma unroll
+      for (int k = 0; k < TT; ++k) {
+        if (16 * k + i < valid) {
+          const int64_t row = t.tok0 + (int64_t)dir * (pos + 16 * k + i);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int64_t at = row * rrow + (int64_t)t.h * E + e0 + 16 * n + 4 * g;
+            const f32x4 x = R[k][n];
+            if (F32 || sw.r_f32) st4(static_cast<float*>(sw.r) + at, x[0], x[1], x[2], x[3]);
+            else st4(static_cast<__bf16*>(sw.r) + at, x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+    }
+
+    if (!last || want_last) {
+      if (valid < C) {
+        set_cz(valid);
+        chunk_decay(valid, gC, gClo);
+      }
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], gC, Z[m][n][r] * gClo);
+      lin_update<A, NW, NT, F32, RT>(Z, ty, zv, cz, g, i);
+    }
+    __syncthreads();
+  }
+
+  if (want_last) {
+    float* dst = STATE ? a.seg_state + ((int64_t)(a.cu ? t.slot + 1 : t.slot + a.N) * a.H + t.h) * A * E
+                       : sw.Z1 + ((int64_t)t.n * a.H + t.h) * A * E;
+#pragma unroll
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = lin_state_row<F32>(m, g, r);
+          if (A >= KU || row < A) dst[(int64_t)row * E + e0 + 16 * n + i] = Z[m][n][r];
+        }
+  }
+}
+
+}  // namespace gdn2

@@ -374,6 +374,97 @@ int gdn2_fwd_chunked_noalloc(const void* q, const void* k, const void* v, const 
                              float* chunk_states, int B, int T, int H, int Dk, int Dv, int chunk,
                              int dt, void* stream);
 
+/*
+ * Linear attention with a decay for each head (retention): the recurrence without the delta rule's erase,
+ *
+ *     S_t = g_h S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t,     g_h = exp(log_decay[h])
+ *
+ * with a constant decay of the head: chunked over prompts and in training, one step for single tokens.
+ *
+ * - q, k [B,T,Hk,Dk]; v, o, dO, dv [B,T,H,Dv]; dq, dk as q, k; all of type dt (outputs and gradients too: rounded
+ *   once, from fp32 sums). States [B,H,Dk,Dv] and log_decay [H] fp32. Packed batches: one row of T tokens with
+ *   cu_seqlens and states [N,H,Dk,Dv] as in gdn2_fwd_varlen, tokens outside every sequence left unwritten.
+ * - H is a multiple of Hk: head h of v and of the states shares the q and k of head h / (H / Hk); dq and dk are
+ *   the sums over the heads that share them (fp32, in a fixed order).
+ * - Dk, Dv in {16, 32, 64, 128}; T >= 0 of any length (T = 0 writes S_final = S0, dS0 = dS_final). The library
+ *   chooses the tiling; it does not change the result beyond the order of fp32 sums.
+ * - log_decay <= 0 as a rule; -inf (g = 0) is exact. Growth (log_decay > 0) follows the formula until fp32
+ *   overflows. The decay is a constant: no gradient with respect to log_decay is formed (a decay for each token
+ *   and head, with its gradient, is gdn2_fwd_chunked_ex's GDN2_FLAG_SCALAR_DECAY).
+ * - An infinity or NaN in a token never reaches an earlier token's output (of gradients: dq's; a later token's dk
+ *   and dv), nor another sequence's; the state it enters is not finite from there on.
+ * - Deterministic, asynchronous on `stream`, no allocation; the general conventions above.
+ *   S0, S_final, dS_final, dS0 are nullable; S_final may be S0, and dS0 may be S0 or dS_final.
+ *   workspace: gdn2_linattn_workspace_bytes(...) bytes, 256-byte aligned (may be NULL where that is 0); calls that
+ *   may overlap need one each.
+ *
+ * gdn2_linattn_bwd_*: gradients of <dO, o> + <dS_final, S_T>. dS0 is formed also when S0 is NULL.
+ *
+ * gdn2_linattn_decode_step: one token for B entries, states updated in place; _slots: entry b's state is
+ * S_pool[slots[b]] ([num_slots,H,Dk,Dv]). An entry whose slot is negative or >= num_slots has no state: its o is
+ * set to zero and nothing else is touched. Entries must name distinct slots.
+ */
+size_t gdn2_linattn_workspace_bytes(int op, int N, int T, int Hk, int H, int Dk, int Dv, int packed, int dt);
+int gdn2_linattn_fwd_chunked(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
+                             void* o, float* S_final, void* workspace, size_t workspace_bytes, int B, int T, int Hk,
+                             int H, int Dk, int Dv, float scale, int dt, void* stream);
+int gdn2_linattn_bwd_chunked(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
+                             const void* dO, const float* dS_final, void* dq, void* dk, void* dv, float* dS0,
+                             void* workspace, size_t workspace_bytes, int B, int T, int Hk, int H, int Dk, int Dv,
+                             float scale, int dt, void* stream);
+int gdn2_linattn_fwd_varlen(const void* q, const void* k, const void* v, const float* log_decay,
+                            const long long* cu_seqlens, int N, const float* S0, void* o, float* S_final,
+                            void* workspace, size_t workspace_bytes, int T, int Hk, int H, int Dk, int Dv, float scale,
+                            int dt, void* stream);
+int gdn2_linattn_bwd_varlen(const void* q, const void* k, const void* v, const float* log_decay,
+                            const long long* cu_seqlens, int N, const float* S0, const void* dO,
+                            const float* dS_final, void* dq, void* dk, void* dv, float* dS0, void* workspace,
+                            size_t workspace_bytes, int T, int Hk, int H, int Dk, int Dv, float scale, int dt,
+                            void* stream);
+int gdn2_linattn_decode_step(const void* q, const void* k, const void* v, const float* log_decay, float* S, void* o,
+                             int B, int Hk, int H, int Dk, int Dv, float scale, int dt, void* stream);
+int gdn2_linattn_decode_step_slots(const void* q, const void* k, const void* v, const float* log_decay, float* S_pool,
+                                   const int* slots, int num_slots, void* o, int B, int Hk, int H, int Dk, int Dv,
+                                   float scale, int dt, void* stream);
+
+/*
+ * gdn2_qk_norm_rope -- the step in front of a mixer: the norm of q and k for each head with the rotation by the
+ * token's position, in one pass (the mixers take q and k as they are).
+ *
+ *     y = R(p) (x r w),   r = (mean(x^2) + eps)^(-1/2)    (GDN2_FLAG_L2_NORM: the sum of squares, not their mean)
+ *
+ * R(p) turns the first `rot` channels in pairs by the angle p inv_freq[j], j = 0 .. rot/2 - 1: channels j and
+ * j + rot/2, with GDN2_FLAG_INTERLEAVED 2j and 2j + 1. q's y is also multiplied by q_scale.
+ *
+ * - q: `tokens` rows of Hq heads x D channels, q_stride elements from row to row, so that q and k can be cut from a
+ *   fused projection's rows; k likewise (k may be NULL with Hk = 0). q_out, k_out: rows q_out_stride, k_out_stride
+ *   apart (Hq D for the contiguous q that the mixers take); q_out may be q with the same stride. Type dt throughout,
+ *   strides multiples of 16 bytes and at least a row. D in {16, 32, 64, 128}; rot a multiple of 16, 0 <= rot <= D.
+ * - q_weight, k_weight [D] fp32, nullable (ones); inv_freq [rot/2] fp32.
+ * - positions int64: row n has positions[n % period] (period = T for positions shared by a batch's rows, else
+ *   tokens); NULL: n % period. Any int64 value; the angle is reduced in fp64, so far positions lose nothing.
+ *
+ * gdn2_qk_norm_rope_bwd: from dq_out, dk_out (contiguous rows, type dt_grad: dt, or GDN2_F32 as the mixers'
+ * backward gives) the gradients dq, dk (type dt, rows q_grad_stride, k_grad_stride apart: the fused projection's
+ * gradient can be written in place) and dq_weight, dk_weight [D] fp32 (nullable; written also for a NULL weight,
+ * as the gradient at ones). workspace: gdn2_qk_norm_rope_workspace_bytes(...) bytes, 256-byte aligned; needed when
+ * a weight's gradient is asked for. tokens = 0 sets the weights' gradients to zero.
+ */
+#define GDN2_FLAG_L2_NORM 16u
+#define GDN2_FLAG_INTERLEAVED 32u
+int gdn2_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                          const long long* positions, const float* inv_freq, void* q_out, void* k_out,
+                          long long tokens, long long period, int Hq, int Hk, int D, int rot, long long q_stride,
+                          long long k_stride, long long q_out_stride, long long k_out_stride, float eps, float q_scale,
+                          int dt, unsigned flags, void* stream);
+size_t gdn2_qk_norm_rope_workspace_bytes(long long tokens, int Hq, int Hk, int D);
+int gdn2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const long long* positions, const float* inv_freq, void* dq, void* dk,
+                          float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                          long long tokens, long long period, int Hq, int Hk, int D, int rot, long long q_stride,
+                          long long k_stride, long long q_grad_stride, long long k_grad_stride, float eps,
+                          float q_scale, int dt, int dt_grad, unsigned flags, void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* gdn2_status_string(int status);
 
