@@ -123,7 +123,7 @@ int forward(const Call& c, void* o, float* S_final) {
   const int G = c.H / c.Hk;
   a.A = c.Dk;
   a.E = c.Dv;
-  a.sw = gdn2::LinSweep{c.q, c.k, c.v, o, G, G, 1, false, false, 1, 1.f, c.scale, c.S0, c.Dv, 1, S_final};
+  a.sw = gdn2::LinSweep{c.q, c.k, c.v, o, G, G, 1, false, false, 1, true, 1.f, c.scale, c.S0, c.Dv, 1, S_final};
   return hip_status(gdn2::launch_linattn_sweep(a, c.stream));
 }
 
@@ -154,19 +154,19 @@ int backward(const Call& c, const void* dO, const float* dS_final, void* dq, voi
   // dq: the forward recurrence of S^T, over (dO, v, k)
   a.A = c.Dv;
   a.E = c.Dk;
-  a.sw = gdn2::LinSweep{dO, c.v, c.k, G == 1 ? dq : partial, 1, 1, G, G > 1, false, 1, 1.f, c.scale,
+  a.sw = gdn2::LinSweep{dO, c.v, c.k, G == 1 ? dq : partial, 1, 1, G, G > 1, false, 1, false, 1.f, c.scale,
                         c.S0, 1, c.Dv, nullptr};
   hipError_t e = gdn2::launch_linattn_sweep(a, c.stream);
   if (e == hipSuccess) e = shared(dq);
   // dk: the reversed recurrence of the state's gradient, transposed, over (v, dO, q)
-  a.sw = gdn2::LinSweep{c.v, dO, c.q, G == 1 ? dk : partial, 1, 1, G, G > 1, true, 0, c.scale, 1.f,
+  a.sw = gdn2::LinSweep{c.v, dO, c.q, G == 1 ? dk : partial, 1, 1, G, G > 1, true, 0, false, c.scale, 1.f,
                         dS_final, 1, c.Dv, nullptr};
   if (e == hipSuccess) e = gdn2::launch_linattn_sweep(a, c.stream);
   if (e == hipSuccess) e = shared(dk);
   // dv: the same state, over (k, q, dO); its last value is dS0
   a.A = c.Dk;
   a.E = c.Dv;
-  a.sw = gdn2::LinSweep{c.k, c.q, dO, dv, G, G, 1, false, true, 0, c.scale, 1.f, dS_final, c.Dv, 1, dS0};
+  a.sw = gdn2::LinSweep{c.k, c.q, dO, dv, G, G, 1, false, true, 0, true, c.scale, 1.f, dS_final, c.Dv, 1, dS0};
   if (e == hipSuccess) e = gdn2::launch_linattn_sweep(a, c.stream);
   return hip_status(e);
 }

@@ -105,7 +105,7 @@ struct LinTile {
   }
 };
 
-// A chunk's rows of one tensor on their way from HBM to LDS: 16 bytes a thread and pass.
+// A chunk's rows of one tensor on their way from HBM to LDS: 16 bytes a thread and pass, NTH threads.
 template <bool F32, int W, int WP, int NTH>
 struct LinFetch {
   using Op = LinOp<F32>;
@@ -113,27 +113,56 @@ struct LinFetch {
   static constexpr int NB = W * Op::ES / 16;              // blocks a row in memory
   static constexpr int TOTAL = NB * Op::C;
   static constexpr int NP = (TOTAL + NTH - 1) / NTH;
+  static constexpr int RP = NTH / NB;                     // rows a pass
+  static_assert(NTH % NB == 0, "a pass takes whole rows");
   uint4 v[NP];
-  // head: this head's first element of token 0; rows pos0.. of the sequence, clamped to its last token
-  __device__ __forceinline__ void load(const char* head, int64_t row_bytes, int64_t tok0, int dir, int pos0, int len) {
+  const char* next;      // this thread's address in the chunk that is fetched next, pass 0
+  int64_t step;          // bytes from row to row of the walk
+  int row, tid;
+  // head: this head's first element of token 0; the walk's row 0 is tok0
+  __device__ __forceinline__ void begin(const char* head, int64_t row_bytes, int64_t tok0, int dir, int pos0, int t) {
+    tid = t;
+    row = t / NB;
+    step = dir * row_bytes;
+    next = head + tok0 * row_bytes + (pos0 + row) * step + (t % NB) * 16;
+  }
+  // the next chunk's rows, `valid` of them in the sequence; rows past them repeat the last
+  __device__ __forceinline__ void load(int valid) {
+    if (valid >= Op::C) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int id = threadIdx.x + p * NTH;
-      const int pos = min(pos0 + id / NB, len - 1);
-      v[p] = *reinterpret_cast<const uint4*>(head + (tok0 + (int64_t)dir * pos) * row_bytes + (id % NB) * 16);
+      for (int p = 0; p < NP; ++p)
+        if (TOTAL % NTH == 0 || row + p * RP < Op::C) v[p] = *reinterpret_cast<const uint4*>(next + p * RP * step);
+    } else {
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        v[p] = *reinterpret_cast<const uint4*>(next + (min(row + p * RP, valid - 1) - row) * step);
     }
+    next += Op::C * step;
   }
   // rows past `valid` are zeros
-  __device__ __forceinline__ void store(char* tile, int valid) const {
+  __device__ __forceinline__ void store(char* tile, int valid) {
+    if (valid < Op::C) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int id = threadIdx.x + p * NTH;
-      const int row = id / NB;
-      if (TOTAL % NTH != 0 && row >= Op::C) break;
-      const bool ok = row < valid;
-      const uint4 z = make_uint4(ok ? v[p].x : 0u, ok ? v[p].y : 0u, ok ? v[p].z : 0u, ok ? v[p].w : 0u);
-      *reinterpret_cast<uint4*>(tile + Tile::at(row, id % NB)) = z;
+      for (int p = 0; p < NP; ++p)
+        if (row + p * RP >= valid) v[p] = make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      if (TOTAL % NTH == 0 || row + p * RP < Op::C)
+        *reinterpret_cast<uint4*>(tile + Tile::at(row + p * RP, tid % NB)) = v[p];
+  }
+  // any element of the valid rows is an infinity or NaN (after store)
+  __device__ __forceinline__ bool non_finite() const {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      if (TOTAL % NTH == 0 || row + p * RP < Op::C) {
+        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // an exponent of all ones carries into the sign's place
+          odd |= F32 ? (w[j] & 0x7f800000u) + 0x00800000u : (w[j] & 0x7f807f80u) + 0x00800080u;
+      }
+    return (odd & (F32 ? 0x80000000u : 0x80008000u)) != 0;
   }
 };
 
@@ -155,20 +184,6 @@ __device__ __forceinline__ bf16x8 pack_rne(const float (&x)[8]) {
   return b;
 }
 
-// any element is an infinity or NaN
-__device__ __forceinline__ bool lin_non_finite(const bf16x8& x) {
-  const u32x4 w = __builtin_bit_cast(u32x4, x);
-  bool odd = false;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f800000u) == 0x7f800000u || (w[j] & 0x7f80u) == 0x7f80u;
-  return odd;
-}
-__device__ __forceinline__ bool lin_non_finite(const f32x4& x) {
-  bool odd = false;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) odd |= (__float_as_uint(x[j]) & 0x7f800000u) == 0x7f800000u;
-  return odd;
-}
 // infinities and NaN replaced by zeros
 __device__ __forceinline__ void lin_finite(bf16x8& x) {
   u32x4 w = __builtin_bit_cast(u32x4, x);
@@ -185,6 +200,8 @@ __device__ __forceinline__ void lin_finite(f32x4& x) {
     if ((__float_as_uint(x[j]) & 0x7f800000u) == 0x7f800000u) x[j] = 0.f;
 }
 
+constexpr int kLinLoad = 4;  // waves that load and form the scores
+
 template <int A, int NW, int NT, bool F32>
 struct LinShape {
   using Op = LinOp<F32>;
@@ -193,8 +210,11 @@ struct LinShape {
   static constexpr int kXY = Op::C * AP * Op::ES;
   static constexpr int kZ = Op::C * CW * Op::ES;
   static constexpr int kP = Op::C * Op::C * Op::ES;
-  static constexpr int kLds = 2 * kXY + kZ + (F32 ? 1 : 2) * kP;
-  static constexpr int kLdsState = kXY + kZ;
+  static constexpr int kThreads = 64 * (NW + kLinLoad);
+  // two buffers of y, z (and x), then the scores, then flags
+  static constexpr int kBuf = kXY + kZ, kBufX = 2 * kXY + kZ;
+  static constexpr int kLds = 2 * kBufX + (F32 ? 1 : 2) * kP + 32;
+  static constexpr int kLdsState = 2 * kBuf;
 };
 
 // What a workgroup has to do. Returns false where there is nothing.
@@ -247,9 +267,10 @@ __device__ __forceinline__ int lin_state_row(int m, int g, int r) {
   return F32 ? 16 * m + 4 * g + r : 32 * (m >> 1) + 8 * g + 4 * (m & 1) + r;
 }
 
-// the token sum of the state update: Z += sum_j y_j (c_j z_j)^T over the chunk in LDS
-template <int A, int NW, int NT, bool F32, int RT>
-__device__ __forceinline__ void lin_update(f32x4 (&Z)[RT][NT], const char* ty, const typename LinOp<F32>::V (&zv)[LinOp<F32>::C / LinOp<F32>::KU][NT],
+// the token sum of the state update: Z += sum_j y_j (c_j z_j)^T over the chunk in LDS. 16 bit: c_j z_j in SPLIT terms
+template <int A, int NW, int NT, bool F32, int SPLIT, int RT>
+__device__ __forceinline__ void lin_update(f32x4 (&Z)[RT][NT], const char* ty,
+                                           const typename LinOp<F32>::V (&zv)[LinOp<F32>::C / LinOp<F32>::KU][NT],
                                            const float (&cz)[LinOp<F32>::C / LinOp<F32>::KU][F32 ? 4 : 8], int g, int i) {
   using Op = LinOp<F32>;
   using TY = LinTile<F32, LinShape<A, NW, NT, F32>::AP>;
@@ -269,50 +290,126 @@ __device__ __forceinline__ void lin_update(f32x4 (&Z)[RT][NT], const char* ty, c
         for (int n = 0; n < NT; ++n) lin_mma(Z[m][n], y, zc[n]);
       }
     } else {
-      bf16x8 z1[NT], z2[NT], z3[NT];
+      bf16x8 zs[SPLIT][NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
-        z1[n] = pack_hi(x);
-        sub_hi(x);
-        z2[n] = pack_hi(x);
-        sub_hi(x);
-        z3[n] = pack_hi(x);
+#pragma unroll
+        for (int t = 0; t + 1 < SPLIT; ++t) {
+          zs[t][n] = pack_hi(x);
+          sub_hi(x);
+        }
+        zs[SPLIT - 1][n] = pack_rne(x);
       }
 #pragma unroll
       for (int m = 0; m < RT; ++m) {
         const bf16x8 y = TY::col(ty, u, g, i, 4 * (m >> 1), 1, m & 1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          lin_mma(Z[m][n], y, z3[n]);
-          lin_mma(Z[m][n], y, z2[n]);
-          lin_mma(Z[m][n], y, z1[n]);
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int t = SPLIT - 1; t >= 0; --t) lin_mma(Z[m][n], y, zs[t][n]);
       }
     }
   }
 }
 
-// STATE: the sum of one piece alone, from a zero state (x, r unused), stored as the entering state of the next
-// piece for the join kernel. Otherwise the sweep of one piece.
+// The loading waves. Step s: the rows of chunk s + 1 go to LDS and chunk s + 2's leave memory; then, with all of
+// chunk s + 1 in LDS, its scores are formed. Chunk 0 comes ahead of the steps.
 template <int A, int NW, int NT, bool F32, bool STATE>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(LinArgs a) {
+struct LinLoader {
   using Sh = LinShape<A, NW, NT, F32>;
   using Op = LinOp<F32>;
   using V = typename Op::V;
-  constexpr int C = Op::C, KU = Op::KU, ES = Op::ES, AP = Sh::AP, CW = Sh::CW, NTH = 64 * NW;
+  static constexpr int C = Op::C, UK = Sh::AP / Op::KU, TT = C / 16;
+  using TX = LinTile<F32, Sh::AP>;
+  using TP = LinTile<F32, C>;
+  LinFetch<F32, A, Sh::AP, 64 * kLinLoad> fx, fy;
+  LinFetch<F32, Sh::CW, Sh::CW, 64 * kLinLoad> fz;
+  float pd[4], pm[4], g16;
+
+  __device__ __forceinline__ void load(int valid) {
+    if constexpr (!STATE) fx.load(valid);
+    fy.load(valid);
+    fz.load(valid);
+  }
+  __device__ __forceinline__ void store(char* buf, int* flags, int w, int valid) {
+    fy.store(buf, valid);
+    fz.store(buf + Sh::kXY, valid);
+    if constexpr (!STATE) {
+      fx.store(buf + Sh::kBuf, valid);
+      const bool odd = __any(fz.non_finite());
+      if (lane_id() == 0) flags[w] = odd;
+    }
+  }
+  // scores, transposed: tile (jt, ts) holds tokens j = 16 jt + 4g + r of columns i = 16 ts + l%16
+  __device__ __forceinline__ void scores(const char* buf, char* tp, int w, int g, int i) {
+    const char* const ty = buf;
+    const char* const tx = buf + Sh::kBuf;
+    const int ts = w;
+    if (ts >= TT) return;
+    V xv[UK];
+#pragma unroll
+    for (int u = 0; u < UK; ++u) xv[u] = TX::row(tx, 16 * ts + i, u, g);
+    float far = 1.f;
+    for (int jt = ts; jt >= 0; --jt) {
+      f32x4 p = zero4();
+#pragma unroll
+      for (int u = 0; u < UK; ++u) lin_mma(p, TX::row(ty, 16 * jt + i, u, g), xv[u]);
+      if (jt == ts) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = i >= 4 * g + r ? p[r] * pd[r] : 0.f;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] *= pm[r] * far;
+        far *= g16;
+      }
+      if constexpr (F32) {
+        *reinterpret_cast<f32x4*>(tp + TP::at(16 * ts + i, 4 * jt + g)) = p;
+      } else {
+        bf16x4 hi, lo;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          hi[r] = f32_to_bf16(p[r]);
+          lo[r] = f32_to_bf16(p[r] - bf16_to_f32(hi[r]));
+        }
+        const int at = TP::at(16 * ts + i, 2 * jt + (g >> 1)) + 8 * (g & 1);
+        *reinterpret_cast<bf16x4*>(tp + at) = hi;
+        *reinterpret_cast<bf16x4*>(tp + Sh::kP + at) = lo;
+      }
+    }
+    if constexpr (!F32) {  // a unit of 32 tokens: the tile past the diagonal of an even strip
+      if ((ts & 1) == 0) {
+        const int at = TP::at(16 * ts + i, 2 * (ts + 1) + (g >> 1)) + 8 * (g & 1);
+        *reinterpret_cast<uint2*>(tp + at) = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(tp + Sh::kP + at) = make_uint2(0u, 0u);
+      }
+    }
+  }
+};
+
+// STATE: the sum of one piece alone, from a zero state (x, r unused), stored as the entering state of the next
+// piece for the join kernel. Otherwise the sweep of one piece.
+//
+// The first NW waves hold the state, the other kLinLoad load and form the scores (which do not depend on the state) a
+// chunk ahead. A step has two halves with a barrier after each: the state's waves form r, then update the state; the
+// loading waves meanwhile write the next chunk to the other buffer, then form its scores.
+template <int A, int NW, int NT, bool F32, bool STATE, int SPLIT>
+__global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
+  using Sh = LinShape<A, NW, NT, F32>;
+  using Op = LinOp<F32>;
+  using V = typename Op::V;
+  constexpr int C = Op::C, KU = Op::KU, ES = Op::ES, AP = Sh::AP, CW = Sh::CW;
   constexpr int RT = AP / 16, UK = AP / KU, UC = C / KU, TT = C / 16, EZ = F32 ? 4 : 8;
+  constexpr int BUF = STATE ? Sh::kBuf : Sh::kBufX;
   using TX = LinTile<F32, AP>;
   using TZ = LinTile<F32, CW>;
   using TP = LinTile<F32, C>;
 
-  extern __shared__ char lds[];
-  char* const ty = lds;
-  char* const tz = lds + Sh::kXY;
-  char* const tx = tz + Sh::kZ;
-  char* const tp = tx + Sh::kXY;  // scores, then (16 bit) what their first bf16 term leaves
+  extern __shared__ char lds[];  // a buffer: y, z, x
+  char* const tp = lds + 2 * BUF;  // scores, then (16 bit) what their first bf16 term leaves
+  int* const flags = reinterpret_cast<int*>(tp + (F32 ? 1 : 2) * Sh::kP);  // [2][kLinLoad]: z has an infinity or NaN
 
   const int ncg = (a.E + CW - 1) / CW;
   int item, cg;
@@ -323,28 +420,66 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
 
   const int l = lane_id(), g = l >> 4, i = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const int e0 = cg * CW + w * 16 * NT;  // this wave's first column
   const LinSweep& sw = a.sw;
   const int dir = sw.rev ? -1 : 1;
   const int E = a.E;
-
-  // heads of the tensors
-  const int hx = t.h / sw.xdiv, hy = t.h / sw.ydiv, hz = t.h / sw.zdiv;
-  const int64_t rbx = (int64_t)(a.H / sw.xdiv) * A * ES, rby = (int64_t)(a.H / sw.ydiv) * A * ES;
-  const int64_t rbz = (int64_t)(a.H / sw.zdiv) * E * ES;
-  const char* const px = static_cast<const char*>(sw.x) + (int64_t)hx * A * ES;
-  const char* const py = static_cast<const char*>(sw.y) + (int64_t)hy * A * ES;
-  const char* const pz = static_cast<const char*>(sw.z) + ((int64_t)hz * E + cg * CW) * ES;
-
-  LinFetch<F32, A, AP, NTH> fx, fy;
-  LinFetch<F32, CW, CW, NTH> fz;
-  if constexpr (!STATE) fx.load(px, rbx, t.tok0, dir, t.pos0, t.len);
-  fy.load(py, rby, t.tok0, dir, t.pos0, t.len);
-  fz.load(pz, rbz, t.tok0, dir, t.pos0, t.len);
-
-  // powers of the decay that a lane needs, the same in every chunk
+  const int steps = (t.pos1 - t.pos0 + C - 1) / C;
   const double l2 = decay_log2(a.log_decay[t.h]);
-  float cz[UC][EZ];  // of the update: token KU u + EZ g + e
+
+  if constexpr (A < AP) {  // the channels that pad x and y to a unit are zero throughout
+    for (int id = threadIdx.x; id < 4 * C * 2; id += Sh::kThreads) {
+      const int row = (id >> 1) & (C - 1), b = 2 + (id & 1), buf = id / (2 * C);
+      if (STATE && buf >= 2) break;
+      char* const tile = lds + (buf & 1) * BUF + (buf >= 2 ? Sh::kBuf : 0);
+      *reinterpret_cast<uint4*>(tile + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
+    }
+  }
+
+  if (w >= NW) {
+    const int lw = w - NW, tid = threadIdx.x - 64 * NW;
+    const int64_t rbx = (int64_t)(a.H / sw.xdiv) * A * ES, rby = (int64_t)(a.H / sw.ydiv) * A * ES;
+    const int64_t rbz = (int64_t)(a.H / sw.zdiv) * E * ES;
+    LinLoader<A, NW, NT, F32, STATE> ld;
+    if constexpr (!STATE)
+      ld.fx.begin(static_cast<const char*>(sw.x) + (int64_t)(t.h / sw.xdiv) * A * ES, rbx, t.tok0, dir, t.pos0, tid);
+    ld.fy.begin(static_cast<const char*>(sw.y) + (int64_t)(t.h / sw.ydiv) * A * ES, rby, t.tok0, dir, t.pos0, tid);
+    ld.fz.begin(static_cast<const char*>(sw.z) + ((int64_t)(t.h / sw.zdiv) * E + cg * CW) * ES, rbz, t.tok0, dir,
+                t.pos0, tid);
+    auto valid = [&](int s) { return min(C, t.pos1 - (t.pos0 + s * C)); };
+    ld.load(valid(0));
+    if constexpr (!STATE) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {  // token i of its tile against token 4g + r of the same tile, of the one before
+        const int d = i - 4 * g - r;
+        ld.pd[r] = d >= 0 ? sw.si * sw.so * decay_pow(l2, d) : 0.f;
+        ld.pm[r] = sw.si * sw.so * decay_pow(l2, 16 + d);
+      }
+      ld.g16 = decay_pow(l2, 16);
+    }
+    ld.store(lds, flags, lw, valid(0));
+    if (steps > 1) ld.load(valid(1));
+    __syncthreads();
+    if constexpr (!STATE) {
+      ld.scores(lds, tp, lw, g, i);
+      __syncthreads();
+    }
+    for (int s = 0; s < steps; ++s) {
+      char* const buf = lds + ((s + 1) & 1) * BUF;
+      if (s + 1 < steps) {
+        ld.store(buf, flags + ((s + 1) & 1) * kLinLoad, lw, valid(s + 1));
+        if (s + 2 < steps) ld.load(valid(s + 2));
+      }
+      __syncthreads();
+      if constexpr (!STATE) {
+        if (s + 1 < steps) ld.scores(buf, tp, lw, g, i);
+        __syncthreads();
+      }
+    }
+    return;
+  }
+
+  const int c0 = w * 16 * NT, e0 = cg * CW + c0;  // this wave's first column in the tile, in the state
+  float cz[UC][EZ];  // powers of the decay in the update, token KU u + EZ g + e
   auto set_cz = [&](int n) {
 #pragma unroll
     for (int u = 0; u < UC; ++u)
@@ -359,15 +494,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
   };
   float gC, gClo;
   chunk_decay(C, gC, gClo);
-  float pd[4], pm[4], g16 = 1.f, ro[TT];
+  float ro[TT];
   if constexpr (!STATE) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {  // scores: token i of its tile against token 4g + r of the same tile, of the one before
-      const int d = i - 4 * g - r;
-      pd[r] = d >= 0 ? sw.si * sw.so * decay_pow(l2, d) : 0.f;
-      pm[r] = sw.si * sw.so * decay_pow(l2, 16 + d);
-    }
-    g16 = decay_pow(l2, 16);
 #pragma unroll
     for (int k = 0; k < TT; ++k) ro[k] = sw.so * decay_pow(l2, 16 * k + i + sw.first);
   }
@@ -400,74 +528,32 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
           }
     }
   }
-  if constexpr (A < AP) {  // the channels that pad x and y to a unit stay zero
-    for (int id = threadIdx.x; id < C * 2; id += NTH) {
-      const int row = id >> 1, b = 2 + (id & 1);
-      *reinterpret_cast<uint4*>(ty + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
-      if constexpr (!STATE) *reinterpret_cast<uint4*>(tx + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
-    }
-  }
+
+  // r: a lane has 4 neighbouring columns of token 16 k + i
+  const int64_t rstep = dir * (int64_t)a.H * E;  // elements from row to row of the walk
+  int64_t rat = t.tok0 * a.H * E + (t.pos0 + i) * rstep + (int64_t)t.h * E + e0 + 4 * g;
 
   const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
-  for (int pos = t.pos0; pos < t.pos1; pos += C) {
-    const int valid = min(C, t.pos1 - pos);
-    const bool last = pos + C >= t.pos1;
-    if constexpr (!STATE) fx.store(tx, valid);
-    fy.store(ty, valid);
-    fz.store(tz, valid);
-    __syncthreads();
-    if (!last) {
-      if constexpr (!STATE) fx.load(px, rbx, t.tok0, dir, pos + C, t.len);
-      fy.load(py, rby, t.tok0, dir, pos + C, t.len);
-      fz.load(pz, rbz, t.tok0, dir, pos + C, t.len);
-    }
+  __syncthreads();
+  if constexpr (!STATE) __syncthreads();
+  for (int s = 0; s < steps; ++s) {
+    const char* const ty = lds + (s & 1) * BUF;
+    const char* const tz = ty + Sh::kXY;
+    const char* const tx = ty + Sh::kBuf;
+    const int valid = min(C, t.pos1 - (t.pos0 + s * C));
+    const bool last = s + 1 == steps;
 
-    f32x4 R[TT][NT];
+    // this wave's columns of z, contraction over tokens
+    V zv[UC][NT];
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        zv[u][n] = F32 ? TZ::col(tz, u, g, i, c0 / 4 + 4 * n, 0, 0) : TZ::col(tz, u, g, i, c0 / 8 + 2 * n, 0, 0);
+
     if constexpr (!STATE) {
-      // scores, transposed: tile (jt, ts) holds tokens j = 16 jt + 4g + r of columns i = 16 ts + l%16
-#pragma unroll
-      for (int s = 0; s < TT / NW + (TT % NW != 0); ++s) {
-        const int ts = w + s * NW;
-        if (TT % NW != 0 && ts >= TT) break;
-        V xv[UK];
-#pragma unroll
-        for (int u = 0; u < UK; ++u) xv[u] = TX::row(tx, 16 * ts + i, u, g);
-        float far = 1.f;
-        for (int jt = ts; jt >= 0; --jt) {
-          f32x4 p = zero4();
-#pragma unroll
-          for (int u = 0; u < UK; ++u) lin_mma(p, TX::row(ty, 16 * jt + i, u, g), xv[u]);
-          if (jt == ts) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p[r] = i >= 4 * g + r ? p[r] * pd[r] : 0.f;
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p[r] *= pm[r] * far;
-            far *= g16;
-          }
-          if constexpr (F32) {
-            *reinterpret_cast<f32x4*>(tp + TP::at(16 * ts + i, 4 * jt + g)) = p;
-          } else {
-            bf16x4 hi, lo;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              hi[r] = f32_to_bf16(p[r]);
-              lo[r] = f32_to_bf16(p[r] - bf16_to_f32(hi[r]));
-            }
-            const int at = TP::at(16 * ts + i, 2 * jt + (g >> 1)) + 8 * (g & 1);
-            *reinterpret_cast<bf16x4*>(tp + at) = hi;
-            *reinterpret_cast<bf16x4*>(tp + Sh::kP + at) = lo;
-          }
-        }
-        if constexpr (!F32) {  // a unit of 32 tokens: the tile past the diagonal of an even strip
-          if ((ts & 1) == 0) {
-            const int at = TP::at(16 * ts + i, 2 * (ts + 1) + (g >> 1)) + 8 * (g & 1);
-            *reinterpret_cast<uint2*>(tp + at) = make_uint2(0u, 0u);
-            *reinterpret_cast<uint2*>(tp + Sh::kP + at) = make_uint2(0u, 0u);
-          }
-        }
-      }
       // r^T from the state: rows are columns of the state, columns are tokens
+      f32x4 R[TT][NT];
 #pragma unroll
       for (int k = 0; k < TT; ++k)
 #pragma unroll
@@ -505,31 +591,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r) R[k][n][r] *= ro[k];
-      __syncthreads();
-    }
 
-    // this wave's columns of z, contraction over tokens
-    V zv[UC][NT];
-#pragma unroll
-    for (int u = 0; u < UC; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        zv[u][n] = F32 ? TZ::col(tz, u, g, i, 4 * (w * NT + n), 0, 0) : TZ::col(tz, u, g, i, 2 * (w * NT + n), 0, 0);
-
-    if constexpr (!STATE) {
       // a zero score times an infinity or NaN of a later token is NaN: such values of z are taken out of the product,
       // and added to their own and later tokens one by one
+      const int4 odd4 = *reinterpret_cast<const int4*>(flags + (s & 1) * kLinLoad);
+      const bool odd = __builtin_amdgcn_readfirstlane(odd4.x | odd4.y | odd4.z | odd4.w) != 0;
       V zp[UC][NT];
-      bool odd = false;
 #pragma unroll
       for (int u = 0; u < UC; ++u)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          zp[u][n] = zv[u][n];
-          odd |= lin_non_finite(zv[u][n]);
-        }
-      const bool any_odd = __any(odd);
-      if (any_odd) {
+        for (int n = 0; n < NT; ++n) zp[u][n] = zv[u][n];
+      if (odd) {
 #pragma unroll
         for (int u = 0; u < UC; ++u)
 #pragma unroll
@@ -549,7 +621,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
           for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zp[u][n], p);
         }
       }
-      if (any_odd) {
+      if (odd) {
 #pragma unroll
         for (int k = 0; k < TT; ++k)
 #pragma unroll
@@ -566,27 +638,26 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
               }
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const int c = 16 * (w * NT + n) + 4 * g + r;
+                const int c = c0 + 16 * n + 4 * g + r;
                 const float z = load1<F32>(tz + TZ::at(j, c * ES / 16), c % (16 / ES));
                 if (j <= 16 * k + i && !(fabsf(z) <= 3.4028235e38f)) R[k][n][r] += p * z;
               }
             }
       }
-      // store: a lane has 4 neighbouring columns of token 16 k + i
-      const int64_t rrow = (int64_t)a.H * E;
 #pragma unroll
       for (int k = 0; k < TT; ++k) {
-        if (16 * k + i < valid) {
-          const int64_t row = t.tok0 + (int64_t)dir * (pos + 16 * k + i);
+        if (valid == C || 16 * k + i < valid) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const int64_t at = row * rrow + (int64_t)t.h * E + e0 + 16 * n + 4 * g;
+            const int64_t at = rat + 16 * k * rstep + 16 * n;
             const f32x4 x = R[k][n];
             if (F32 || sw.r_f32) st4(static_cast<float*>(sw.r) + at, x[0], x[1], x[2], x[3]);
             else st4(static_cast<__bf16*>(sw.r) + at, x[0], x[1], x[2], x[3]);
           }
         }
       }
+      rat += C * rstep;
+      __syncthreads();
     }
 
     if (!last || want_last) {
@@ -600,7 +671,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void gdn2_linattn_kernel(
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], gC, Z[m][n][r] * gClo);
-      lin_update<A, NW, NT, F32, RT>(Z, ty, zv, cz, g, i);
+      lin_update<A, NW, NT, F32, SPLIT, RT>(Z, ty, zv, cz, g, i);
     }
     __syncthreads();
   }
