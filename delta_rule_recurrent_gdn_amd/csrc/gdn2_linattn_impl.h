@@ -211,9 +211,10 @@ struct LinShape {
   static constexpr int kZ = Op::C * CW * Op::ES;
   static constexpr int kP = Op::C * Op::C * Op::ES;
   static constexpr int kThreads = 64 * (NW + kLinLoad);
-  // two buffers of y, z (and x), then the scores, then flags
-  static constexpr int kBuf = kXY + kZ, kBufX = 2 * kXY + kZ;
-  static constexpr int kLds = 2 * kBufX + (F32 ? 1 : 2) * kP + 32;
+  static constexpr int kBuf = kXY + kZ, kBufX = 2 * kXY + kZ;  // y, z; y, z, x
+  static constexpr int kScores = (F32 ? 1 : 2) * kP;
+  // three buffers of a chunk's rows, two of its scores, flags; the sums of the pieces: two buffers
+  static constexpr int kLds = 3 * kBufX + 2 * kScores + 3 * 4 * kLinLoad;
   static constexpr int kLdsState = 2 * kBuf;
 };
 
@@ -304,19 +305,22 @@ __device__ __forceinline__ void lin_update(f32x4 (&Z)[RT][NT], const char* ty,
         zs[SPLIT - 1][n] = pack_rne(x);
       }
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        const bf16x8 y = TY::col(ty, u, g, i, 4 * (m >> 1), 1, m & 1);
+      for (int m = 0; m < RT; m += 2) {  // two tiles in turn: the terms of one sum wait for one another
+        const bf16x8 y0 = TY::col(ty, u, g, i, 4 * (m >> 1), 1, 0);
+        const bf16x8 y1 = TY::col(ty, u, g, i, 4 * (m >> 1), 1, 1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int t = SPLIT - 1; t >= 0; --t)
 #pragma unroll
-          for (int t = SPLIT - 1; t >= 0; --t) lin_mma(Z[m][n], y, zs[t][n]);
+          for (int n = 0; n < NT; ++n) {
+            lin_mma(Z[m][n], y0, zs[t][n]);
+            lin_mma(Z[m + 1][n], y1, zs[t][n]);
+          }
       }
     }
   }
 }
 
-// The loading waves. Step s: the rows of chunk s + 1 go to LDS and chunk s + 2's leave memory; then, with all of
-// chunk s + 1 in LDS, its scores are formed. Chunk 0 comes ahead of the steps.
+// The loading waves: the rows of a chunk from memory to LDS, and the scores of a chunk in LDS.
 template <int A, int NW, int NT, bool F32, bool STATE>
 struct LinLoader {
   using Sh = LinShape<A, NW, NT, F32>;
@@ -343,27 +347,39 @@ struct LinLoader {
       if (lane_id() == 0) flags[w] = odd;
     }
   }
+  // The n-th score tile of wave w, strip ts against strip jt <= ts, at most three a wave:
+  //   w = 0: (3,3) (3,2)   1: (3,1) (3,0) (0,0)   2: (2,2) (2,1) (2,0)   3: (1,1) (1,0)      (chunks of four strips)
+  //   w = 0: (1,1)         1: (1,0)               2: (0,0)                                  (two strips)
+  __device__ __forceinline__ static bool tile(int w, int n, int& ts, int& jt) {
+    if constexpr (TT == 4) {
+      ts = w == 0 ? 3 : w == 1 ? (n < 2 ? 3 : 0) : 4 - w;
+      jt = w == 0 ? 3 - n : w == 1 ? (n < 2 ? 1 - n : 0) : 4 - w - n;
+      return n < 2 || w == 1 || w == 2;
+    } else {
+      ts = w < 2 ? 1 : 0;
+      jt = w == 0 ? 1 : 0;
+      return n == 0 && w < 3;
+    }
+  }
   // scores, transposed: tile (jt, ts) holds tokens j = 16 jt + 4g + r of columns i = 16 ts + l%16
   __device__ __forceinline__ void scores(const char* buf, char* tp, int w, int g, int i) {
     const char* const ty = buf;
     const char* const tx = buf + Sh::kBuf;
-    const int ts = w;
-    if (ts >= TT) return;
-    V xv[UK];
 #pragma unroll
-    for (int u = 0; u < UK; ++u) xv[u] = TX::row(tx, 16 * ts + i, u, g);
-    float far = 1.f;
-    for (int jt = ts; jt >= 0; --jt) {
-      f32x4 p = zero4();
+    for (int n = 0; n < (TT == 4 ? 3 : 1); ++n) {
+      int ts, jt;
+      if (!tile(w, n, ts, jt)) break;
+      f32x4 p = zero4(), p2 = zero4();  // two sums side by side: half the wait for one another
 #pragma unroll
-      for (int u = 0; u < UK; ++u) lin_mma(p, TX::row(ty, 16 * jt + i, u, g), xv[u]);
-      if (jt == ts) {
+      for (int u = 0; u < UK; ++u)
+        lin_mma((u & 1) ? p2 : p, TX::row(ty, 16 * jt + i, u, g), TX::row(tx, 16 * ts + i, u, g));
+      if (ts == jt) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] = i >= 4 * g + r ? p[r] * pd[r] : 0.f;
+        for (int r = 0; r < 4; ++r) p[r] = i >= 4 * g + r ? (p[r] + p2[r]) * pd[r] : 0.f;
       } else {
+        const float far = ts - jt == 1 ? 1.f : ts - jt == 2 ? g16 : g16 * g16;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] *= pm[r] * far;
-        far *= g16;
+        for (int r = 0; r < 4; ++r) p[r] = (p[r] + p2[r]) * (pm[r] * far);
       }
       if constexpr (F32) {
         *reinterpret_cast<f32x4*>(tp + TP::at(16 * ts + i, 4 * jt + g)) = p;
@@ -377,13 +393,11 @@ struct LinLoader {
         const int at = TP::at(16 * ts + i, 2 * jt + (g >> 1)) + 8 * (g & 1);
         *reinterpret_cast<bf16x4*>(tp + at) = hi;
         *reinterpret_cast<bf16x4*>(tp + Sh::kP + at) = lo;
-      }
-    }
-    if constexpr (!F32) {  // a unit of 32 tokens: the tile past the diagonal of an even strip
-      if ((ts & 1) == 0) {
-        const int at = TP::at(16 * ts + i, 2 * (ts + 1) + (g >> 1)) + 8 * (g & 1);
-        *reinterpret_cast<uint2*>(tp + at) = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(tp + Sh::kP + at) = make_uint2(0u, 0u);
+        if (ts == jt && (ts & 1) == 0) {  // a unit of 32 tokens: the tile past the diagonal of an even strip
+          const int past = TP::at(16 * ts + i, 2 * (ts + 1) + (g >> 1)) + 8 * (g & 1);
+          *reinterpret_cast<uint2*>(tp + past) = make_uint2(0u, 0u);
+          *reinterpret_cast<uint2*>(tp + Sh::kP + past) = make_uint2(0u, 0u);
+        }
       }
     }
   }
@@ -392,9 +406,9 @@ struct LinLoader {
 // STATE: the sum of one piece alone, from a zero state (x, r unused), stored as the entering state of the next
 // piece for the join kernel. Otherwise the sweep of one piece.
 //
-// The first NW waves hold the state, the other kLinLoad load and form the scores (which do not depend on the state) a
-// chunk ahead. A step has two halves with a barrier after each: the state's waves form r, then update the state; the
-// loading waves meanwhile write the next chunk to the other buffer, then form its scores.
+// The first NW waves hold the state, the other kLinLoad work ahead of them: in the step in which the state's waves take
+// chunk s, they form the scores of chunk s + 1 (which do not depend on the state), write chunk s + 2 to LDS and send
+// for chunk s + 3, with one barrier a step. (STATE: no scores, chunk s + 1 to LDS, s + 2 sent for.)
 template <int A, int NW, int NT, bool F32, bool STATE, int SPLIT>
 __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
   using Sh = LinShape<A, NW, NT, F32>;
@@ -408,8 +422,8 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   using TP = LinTile<F32, C>;
 
   extern __shared__ char lds[];  // a buffer: y, z, x
-  char* const tp = lds + 2 * BUF;  // scores, then (16 bit) what their first bf16 term leaves
-  int* const flags = reinterpret_cast<int*>(tp + (F32 ? 1 : 2) * Sh::kP);  // [2][kLinLoad]: z has an infinity or NaN
+  char* const scores = lds + 3 * BUF;  // scores, then (16 bit) what their first bf16 term leaves
+  int* const flags = reinterpret_cast<int*>(scores + 2 * Sh::kScores);  // [3][kLinLoad]: z has an infinity or NaN
 
   const int ncg = (a.E + CW - 1) / CW;
   int item, cg;
@@ -427,11 +441,11 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   const double l2 = decay_log2(a.log_decay[t.h]);
 
   if constexpr (A < AP) {  // the channels that pad x and y to a unit are zero throughout
-    for (int id = threadIdx.x; id < 4 * C * 2; id += Sh::kThreads) {
-      const int row = (id >> 1) & (C - 1), b = 2 + (id & 1), buf = id / (2 * C);
-      if (STATE && buf >= 2) break;
-      char* const tile = lds + (buf & 1) * BUF + (buf >= 2 ? Sh::kBuf : 0);
-      *reinterpret_cast<uint4*>(tile + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
+    constexpr int tiles = STATE ? 2 : 6;
+    for (int id = threadIdx.x; id < tiles * C * 2; id += Sh::kThreads) {
+      const int row = (id >> 1) & (C - 1), b = 2 + (id & 1), tile = id / (2 * C);
+      char* const at = STATE ? lds + tile * BUF : lds + (tile >> 1) * BUF + (tile & 1) * Sh::kBuf;
+      *reinterpret_cast<uint4*>(at + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
     }
   }
 
@@ -458,20 +472,26 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     }
     ld.store(lds, flags, lw, valid(0));
     if (steps > 1) ld.load(valid(1));
-    __syncthreads();
-    if constexpr (!STATE) {
-      ld.scores(lds, tp, lw, g, i);
+    if constexpr (STATE) {
       __syncthreads();
-    }
-    for (int s = 0; s < steps; ++s) {
-      char* const buf = lds + ((s + 1) & 1) * BUF;
-      if (s + 1 < steps) {
-        ld.store(buf, flags + ((s + 1) & 1) * kLinLoad, lw, valid(s + 1));
+      for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) ld.store(lds + ((s + 1) & 1) * BUF, flags, lw, valid(s + 1));
         if (s + 2 < steps) ld.load(valid(s + 2));
+        __syncthreads();
       }
+    } else {
+      if (steps > 1) ld.store(lds + BUF, flags + kLinLoad, lw, valid(1));
+      if (steps > 2) ld.load(valid(2));
       __syncthreads();
-      if constexpr (!STATE) {
-        if (s + 1 < steps) ld.scores(buf, tp, lw, g, i);
+      ld.scores(lds, scores, lw, g, i);
+      __syncthreads();
+      int next = 1, after = 2;  // buffers of chunks s + 1, s + 2
+      for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) ld.scores(lds + next * BUF, scores + ((s + 1) & 1) * Sh::kScores, lw, g, i);
+        if (s + 2 < steps) ld.store(lds + after * BUF, flags + after * kLinLoad, lw, valid(s + 2));
+        if (s + 3 < steps) ld.load(valid(s + 3));
+        next = after;
+        after = after == 2 ? 0 : after + 1;
         __syncthreads();
       }
     }
@@ -536,8 +556,10 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
   __syncthreads();
   if constexpr (!STATE) __syncthreads();
+  int now = 0;  // this chunk's buffer
   for (int s = 0; s < steps; ++s) {
-    const char* const ty = lds + (s & 1) * BUF;
+    const char* const ty = lds + now * BUF;
+    const char* const tp = scores + (s & 1) * Sh::kScores;
     const char* const tz = ty + Sh::kXY;
     const char* const tx = ty + Sh::kBuf;
     const int valid = min(C, t.pos1 - (t.pos0 + s * C));
@@ -558,8 +580,16 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       for (int k = 0; k < TT; ++k)
 #pragma unroll
         for (int n = 0; n < NT; ++n) R[k][n] = zero4();
+      V xv[TT];
+#pragma unroll
+      for (int k = 0; k < TT; ++k) xv[k] = TX::row(tx, 16 * k + i, 0, g);
 #pragma unroll
       for (int u = 0; u < UK; ++u) {
+        V xn[TT];
+        if (u + 1 < UK) {
+#pragma unroll
+          for (int k = 0; k < TT; ++k) xn[k] = TX::row(tx, 16 * k + i, u + 1, g);
+        }
         V zh[NT];
         V zl[NT];
 #pragma unroll
@@ -576,14 +606,17 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
           }
         }
 #pragma unroll
-        for (int k = 0; k < TT; ++k) {
-          const V xv = TX::row(tx, 16 * k + i, u, g);
+        for (int k = 0; k < TT; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if constexpr (!F32) lin_mma(R[k][n], zl[n], xv);
-            lin_mma(R[k][n], zh[n], xv);
-          }
+          for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zh[n], xv[k]);
+        if constexpr (!F32) {
+#pragma unroll
+          for (int k = 0; k < TT; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zl[n], xv[k]);
         }
+#pragma unroll
+        for (int k = 0; k < TT; ++k) xv[k] = xn[k];
       }
 #pragma unroll
       for (int k = 0; k < TT; ++k)
@@ -594,7 +627,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 
       // a zero score times an infinity or NaN of a later token is NaN: such values of z are taken out of the product,
       // and added to their own and later tokens one by one
-      const int4 odd4 = *reinterpret_cast<const int4*>(flags + (s & 1) * kLinLoad);
+      const int4 odd4 = *reinterpret_cast<const int4*>(flags + now * kLinLoad);
       const bool odd = __builtin_amdgcn_readfirstlane(odd4.x | odd4.y | odd4.z | odd4.w) != 0;
       V zp[UC][NT];
 #pragma unroll
@@ -657,7 +690,6 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
         }
       }
       rat += C * rstep;
-      __syncthreads();
     }
 
     if (!last || want_last) {
@@ -673,6 +705,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
           for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], gC, Z[m][n][r] * gClo);
       lin_update<A, NW, NT, F32, SPLIT, RT>(Z, ty, zv, cz, g, i);
     }
+    now = now == (STATE ? 1 : 2) ? 0 : now + 1;
     __syncthreads();
   }
 
