@@ -268,58 +268,6 @@ __device__ __forceinline__ int lin_state_row(int m, int g, int r) {
   return F32 ? 16 * m + 4 * g + r : 32 * (m >> 1) + 8 * g + 4 * (m & 1) + r;
 }
 
-// the token sum of the state update: Z += sum_j y_j (c_j z_j)^T over the chunk in LDS. 16 bit: c_j z_j in SPLIT terms
-template <int A, int NW, int NT, bool F32, int SPLIT, int RT>
-__device__ __forceinline__ void lin_update(f32x4 (&Z)[RT][NT], const char* ty,
-                                           const typename LinOp<F32>::V (&zv)[LinOp<F32>::C / LinOp<F32>::KU][NT],
-                                           const float (&cz)[LinOp<F32>::C / LinOp<F32>::KU][F32 ? 4 : 8], int g, int i) {
-  using Op = LinOp<F32>;
-  using TY = LinTile<F32, LinShape<A, NW, NT, F32>::AP>;
-  constexpr int UC = Op::C / Op::KU;
-#pragma unroll
-  for (int u = 0; u < UC; ++u) {
-    if constexpr (F32) {
-      f32x4 zc[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) zc[n][e] = cz[u][e] * zv[u][n][e];
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        const f32x4 y = TY::col(ty, u, g, i, 4 * m, 0, 0);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) lin_mma(Z[m][n], y, zc[n]);
-      }
-    } else {
-      bf16x8 zs[SPLIT][NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
-#pragma unroll
-        for (int t = 0; t + 1 < SPLIT; ++t) {
-          zs[t][n] = pack_hi(x);
-          sub_hi(x);
-        }
-        zs[SPLIT - 1][n] = pack_rne(x);
-      }
-#pragma unroll
-      for (int m = 0; m < RT; m += 2) {  // two tiles in turn: the terms of one sum wait for one another
-        const bf16x8 y0 = TY::col(ty, u, g, i, 4 * (m >> 1), 1, 0);
-        const bf16x8 y1 = TY::col(ty, u, g, i, 4 * (m >> 1), 1, 1);
-#pragma unroll
-        for (int t = SPLIT - 1; t >= 0; --t)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            lin_mma(Z[m][n], y0, zs[t][n]);
-            lin_mma(Z[m + 1][n], y1, zs[t][n]);
-          }
-      }
-    }
-  }
-}
-
 // The loading waves: the rows of a chunk from memory to LDS, and the scores of a chunk in LDS.
 template <int A, int NW, int NT, bool F32, bool STATE>
 struct LinLoader {
@@ -507,13 +455,16 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       for (int e = 0; e < EZ; ++e) cz[u][e] = sw.si * decay_pow(l2, max(0, n - sw.first - (KU * u + EZ * g + e)));
   };
   set_cz(C);
-  auto chunk_decay = [&](int n, float& hi, float& lo) {  // g^n as a sum of two floats: it multiplies the state again and again
+  // g^n, and what rounding left of it, relative: a state decays by the same rounded g^C again and again, so the rest
+  // is made up for every kMakeUp chunks
+  constexpr int kMakeUp = 8;
+  auto chunk_decay = [&](int n, float& hi, float& rest) {
     const double x = exp2(l2 * n);
     hi = (float)x;
-    lo = (float)(x - hi);
+    rest = hi > 0.f ? (float)((x - hi) / x) : 0.f;
   };
-  float gC, gClo;
-  chunk_decay(C, gC, gClo);
+  float gC, gRest;
+  chunk_decay(C, gC, gRest);
   float ro[TT];
   if constexpr (!STATE) {
 #pragma unroll
@@ -554,42 +505,73 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   int64_t rat = t.tok0 * a.H * E + (t.pos0 + i) * rstep + (int64_t)t.h * E + e0 + 4 * g;
 
   const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
-  __syncthreads();
-  if constexpr (!STATE) __syncthreads();
-  int now = 0;  // this chunk's buffer
-  for (int s = 0; s < steps; ++s) {
-    const char* const ty = lds + now * BUF;
-    const char* const tp = scores + (s & 1) * Sh::kScores;
-    const char* const tz = ty + Sh::kXY;
-    const char* const tx = ty + Sh::kBuf;
-    const int valid = min(C, t.pos1 - (t.pos0 + s * C));
-    const bool last = s + 1 == steps;
-
-    // this wave's columns of z, contraction over tokens
-    V zv[UC][NT];
+  // Operands are read from LDS a stage ahead of their products, which the fences keep apart.
+#define GDN2_LIN_FENCE __builtin_amdgcn_sched_barrier(0)
+  V zv[UC][NT];  // this wave's columns of z, contraction over tokens
+  V xv[TT];      // rows of x, unit 0
+  auto fetch = [&](const char* buf) {
 #pragma unroll
     for (int u = 0; u < UC; ++u)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        zv[u][n] = F32 ? TZ::col(tz, u, g, i, c0 / 4 + 4 * n, 0, 0) : TZ::col(tz, u, g, i, c0 / 8 + 2 * n, 0, 0);
+        zv[u][n] = TZ::col(buf + Sh::kXY, u, g, i, F32 ? c0 / 4 + 4 * n : c0 / 8 + 2 * n, 0, 0);
+    if constexpr (!STATE) {
+#pragma unroll
+      for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
+    }
+  };
+  constexpr int MP = RT >= 2 ? 2 : 1, NS = UC * RT / MP;  // tiles a stage of the update, its stages
+  auto y_of = [&](const char* ty, int st, int m) {        // operand of stage st, its tile m
+    const int u = st / (RT / MP), mt = st % (RT / MP) * MP + m;
+    return F32 ? TX::col(ty, u, g, i, 4 * mt, 0, 0) : TX::col(ty, u, g, i, 4 * (mt >> 1), 1, mt & 1);
+  };
+  __syncthreads();
+  if constexpr (!STATE) __syncthreads();
+  int now = 0;  // this chunk's buffer
+  fetch(lds);
+  for (int s = 0; s < steps; ++s) {
+    const char* const ty = lds + now * BUF;
+    const char* const tz = ty + Sh::kXY;
+    const char* const tx = ty + Sh::kBuf;
+    const char* const tp = scores + (s & 1) * Sh::kScores;
+    const int valid = min(C, t.pos1 - (t.pos0 + s * C));
+    const bool last = s + 1 == steps;
+    now = now == (STATE ? 1 : 2) ? 0 : now + 1;
+    const char* const after = lds + now * BUF;
+    V y[3][MP];
 
     if constexpr (!STATE) {
+      // scores by unit: row tile k, unit u <= 16 k / KU
+      constexpr int NU = F32 ? TT * (TT + 1) / 2 : TT * (TT + 2) / 4, H1 = NU / 2;
+      V ph[NU], pl[F32 ? 1 : NU];
+      auto get_scores = [&](int from, int to) {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < TT; ++k)
+#pragma unroll
+          for (int u = 0; u <= 16 * k / KU; ++u, ++n)
+            if (n >= from && n < to) {
+              ph[n] = TP::row(tp, 16 * k + i, u, g);
+              if constexpr (!F32) pl[n] = TP::row(tp + Sh::kP, 16 * k + i, u, g);
+            }
+      };
+      const int4 odd4 = *reinterpret_cast<const int4*>(flags + (now == 0 ? 2 : now - 1) * kLinLoad);
       // r^T from the state: rows are columns of the state, columns are tokens
       f32x4 R[TT][NT];
 #pragma unroll
       for (int k = 0; k < TT; ++k)
 #pragma unroll
         for (int n = 0; n < NT; ++n) R[k][n] = zero4();
-      V xv[TT];
-#pragma unroll
-      for (int k = 0; k < TT; ++k) xv[k] = TX::row(tx, 16 * k + i, 0, g);
 #pragma unroll
       for (int u = 0; u < UK; ++u) {
         V xn[TT];
         if (u + 1 < UK) {
 #pragma unroll
           for (int k = 0; k < TT; ++k) xn[k] = TX::row(tx, 16 * k + i, u + 1, g);
+        } else {
+          get_scores(0, H1);
         }
+        GDN2_LIN_FENCE;
         V zh[NT];
         V zl[NT];
 #pragma unroll
@@ -615,19 +597,15 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
             for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zl[n], xv[k]);
         }
+        GDN2_LIN_FENCE;
+        if (u + 1 < UK) {
 #pragma unroll
-        for (int k = 0; k < TT; ++k) xv[k] = xn[k];
+          for (int k = 0; k < TT; ++k) xv[k] = xn[k];
+        }
       }
-#pragma unroll
-      for (int k = 0; k < TT; ++k)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) R[k][n][r] *= ro[k];
 
       // a zero score times an infinity or NaN of a later token is NaN: such values of z are taken out of the product,
       // and added to their own and later tokens one by one
-      const int4 odd4 = *reinterpret_cast<const int4*>(flags + now * kLinLoad);
       const bool odd = __builtin_amdgcn_readfirstlane(odd4.x | odd4.y | odd4.z | odd4.w) != 0;
       V zp[UC][NT];
 #pragma unroll
@@ -640,20 +618,37 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
           for (int n = 0; n < NT; ++n) lin_finite(zp[u][n]);
       }
+      get_scores(H1, NU);
+      GDN2_LIN_FENCE;
 #pragma unroll
-      for (int k = 0; k < TT; ++k) {
+      for (int k = 0; k < TT; ++k)
 #pragma unroll
-        for (int u = 0; u <= (16 * k) / KU; ++u) {
-          const V p = TP::row(tp, 16 * k + i, u, g);
-          if constexpr (!F32) {
-            const V pl = TP::row(tp + Sh::kP, 16 * k + i, u, g);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zp[u][n], pl);
-          }
+          for (int r = 0; r < 4; ++r) R[k][n][r] *= ro[k];
+      auto add_scores = [&](int from, int to) {
+        int n = 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zp[u][n], p);
-        }
+        for (int k = 0; k < TT; ++k)
+#pragma unroll
+          for (int u = 0; u <= 16 * k / KU; ++u, ++n)
+            if (n >= from && n < to) {
+#pragma unroll
+              for (int c = 0; c < NT; ++c) {
+                if constexpr (!F32) lin_mma(R[k][c], zp[u][c], pl[n]);
+                lin_mma(R[k][c], zp[u][c], ph[n]);
+              }
+            }
+      };
+      add_scores(0, H1);
+      GDN2_LIN_FENCE;
+#pragma unroll
+      for (int m = 0; m < MP; ++m) {
+        y[0][m] = y_of(ty, 0, m);
+        if (NS > 1) y[1][m] = y_of(ty, 1, m);
       }
+      GDN2_LIN_FENCE;
+      add_scores(H1, NU);
       if (odd) {
 #pragma unroll
         for (int k = 0; k < TT; ++k)
@@ -690,24 +685,83 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
         }
       }
       rat += C * rstep;
+    } else {
+#pragma unroll
+      for (int m = 0; m < MP; ++m) {
+        y[0][m] = y_of(ty, 0, m);
+        if (NS > 1) y[1][m] = y_of(ty, 1, m);
+      }
     }
 
     if (!last || want_last) {
       if (valid < C) {
         set_cz(valid);
-        chunk_decay(valid, gC, gClo);
+        chunk_decay(valid, gC, gRest);
       }
+      if (valid < C || s % kMakeUp == kMakeUp - 1) {
+        const float rest = valid < C ? gRest : kMakeUp * gRest;
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+        for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], gC, Z[m][n][r] * gClo);
-      lin_update<A, NW, NT, F32, SPLIT, RT>(Z, ty, zv, cz, g, i);
+            for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], rest, Z[m][n][r]);
+      }
+      // Z <- g^n Z + sum_j y_j (c_j z_j)^T. 16 bit: c_j z_j in SPLIT terms
+      V zs[F32 ? 1 : SPLIT][NT];
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        if (st + 2 < NS) {
+#pragma unroll
+          for (int m = 0; m < MP; ++m) y[(st + 2) % 3][m] = y_of(ty, st + 2, m);
+        }
+        GDN2_LIN_FENCE;
+        const int u = st / (RT / MP), m0 = st % (RT / MP) * MP;
+        if (m0 == 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (F32) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) zs[0][n][e] = cz[u][e] * zv[u][n][e];
+            } else {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
+#pragma unroll
+              for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
+                zs[t2][n] = pack_hi(x);
+                sub_hi(x);
+              }
+              zs[SPLIT - 1][n] = pack_rne(x);
+            }
+          }
+        }
+        if (u == 0) {
+#pragma unroll
+          for (int m = 0; m < MP; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) Z[m0 + m][n][r] *= gC;
+        }
+#pragma unroll
+        for (int t2 = (F32 ? 1 : SPLIT) - 1; t2 >= 0; --t2)
+#pragma unroll
+          for (int m = 0; m < MP; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) lin_mma(Z[m0 + m][n], y[st % 3][m], zs[t2][n]);
+        GDN2_LIN_FENCE;
+      }
     }
-    now = now == (STATE ? 1 : 2) ? 0 : now + 1;
-    __syncthreads();
+    if constexpr (!STATE) {  // the next chunk is in LDS since the step before
+      if (!last) fetch(after);
+      __syncthreads();
+    } else {
+      __syncthreads();
+      if (!last) fetch(after);
+    }
   }
+#undef GDN2_LIN_FENCE
 
   if (want_last) {
     float* dst = STATE ? a.seg_state + ((int64_t)(a.cu ? t.slot + 1 : t.slot + a.N) * a.H + t.h) * A * E
