@@ -61,29 +61,58 @@ __device__ __forceinline__ void lin_mma(f32x4& acc, const f32x4& a, const f32x4&
   for (int i = 0; i < 4; ++i) acc = mfma16x16x4(a[i], b[i], acc);
 }
 
-// A tile [rows][W] of the inputs' type in LDS, 16-byte blocks permuted within a row so that neither a wave's
-// 16-byte reads down a column of blocks nor its transposing (fp32: 4-byte) reads across rows meet in a bank.
-template <bool F32, int W>
+// A tile [rows][W] of the inputs' type in LDS: row after row, the 16-byte blocks of a row permuted so that what the
+// lanes served together touch lies in different banks (64 of 4 bytes for reads: 16 blocks wide; 16-byte reads are
+// served 16 lanes at a time, 8-byte ones 32, 4-byte ones 64). How a tile is read decides which bits of the row go
+// where; rows narrower than 16 blocks share the banks' width, which separates their lowest bits already:
+//   kRows: 16 bytes of 16 neighbouring rows (x, the scores);
+//   kBoth: 16 bit: 8 bytes of rows 0-3 and 8-11 of 16, in 4 neighbouring blocks each (the transposing read), and
+//          8 bytes of 16 neighbouring rows, in 2 blocks; one bit exchanges the halves of a block (y);
+//   kCols: 16 bit: 32 bytes of rows 0-3 and 8-11 (z).
+// fp32 reads down the rows 4 bytes wide: 16 columns of rows 4 apart.
+enum LinUse { kRows, kBoth, kCols };
+
+template <bool F32, int W, LinUse USE>
 struct LinTile {
   using Op = LinOp<F32>;
+  using V = typename Op::V;
   static constexpr int kRow = W * Op::ES;       // bytes a row
   static constexpr int NB = kRow / 16;          // blocks a row
+  static constexpr bool kSwap = !F32 && USE == kBoth;
+  __device__ __forceinline__ static int bit(int r, int from, int to) { return ((r >> from) & 1) << to; }
   __device__ __forceinline__ static int perm(int r) {
-    if constexpr (NB >= 16) return F32 ? (r & 15) : (((r & 3) << 2) | ((r >> 2) & 3));
-    else if constexpr (NB == 8) return F32 ? ((r >> 1) & 7) : ((((r >> 1) & 1) << 2) | ((r >> 2) & 3));
-    else if constexpr (NB == 4) return (r >> 2) & 3;
-    else return 0;
+    if constexpr (F32) return NB >= 16 ? (r & 15) : NB == 8 ? bit(r, 2, 2) | bit(r, 3, 1) | bit(r, 1, 0) : (r >> 2) & 3;
+    else if constexpr (USE == kRows) return NB >= 16 ? (r & 15) : NB == 8 ? (r >> 1) & 7 : (r >> 2) & 3;
+    else if constexpr (USE == kBoth)
+      return NB >= 16 ? bit(r, 3, 3) | bit(r, 0, 2) | bit(r, 2, 1) : NB == 8 ? bit(r, 3, 2) | bit(r, 2, 1) : bit(r, 2, 1);
+    else
+      return NB >= 16 ? bit(r, 3, 3) | bit(r, 1, 2) | bit(r, 0, 1) : NB == 8 ? bit(r, 3, 2) | bit(r, 1, 1)
+             : NB == 4 ? bit(r, 3, 1) : 0;
   }
-  // byte offset of block b of row r
+  __device__ __forceinline__ static bool swapped(int r) { return kSwap && ((r >> (NB >= 8 ? 1 : 3)) & 1); }
+  // byte offset of block b of row r, of its 8-byte half h
   __device__ __forceinline__ static int at(int r, int b) { return r * kRow + ((b ^ perm(r)) << 4); }
-  // operand of unit u from row r (contraction along the row), lane group g
-  __device__ __forceinline__ static typename Op::V row(const char* t, int r, int u, int g) {
-    return *reinterpret_cast<const typename Op::V*>(t + at(r, 4 * u + g));
+  __device__ __forceinline__ static int at(int r, int b, int h) { return at(r, b) + ((h ^ (int)swapped(r)) << 3); }
+  __device__ __forceinline__ static void put(char* t, int r, int b, uint4 v) {
+    const bool x = swapped(r);
+    *reinterpret_cast<uint4*>(t + at(r, b)) =
+        make_uint4(x ? v.z : v.x, x ? v.w : v.y, x ? v.x : v.z, x ? v.y : v.w);
   }
-  // operand whose contraction runs down the rows 16-bit: 32u + 8g .. + 7, fp32: 16u + 4g .. + 3; its 16 columns are
-  // for lane l%16 = 4p + e: 16 bit: block b0 + p * bs, elements h..h+3 (four columns a 16-byte block's half), fp32:
-  // column 4 b0 + l%16
-  __device__ __forceinline__ static typename Op::V col(const char* t, int u, int g, int i, int b0, int bs, int h) {
+  // operand of unit u from row r (contraction along the row), lane group g
+  __device__ __forceinline__ static V row(const char* t, int r, int u, int g) {
+    if constexpr (kSwap) {
+      const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + at(r, 4 * u + g, 0));
+      const bf16x4 hi = *reinterpret_cast<const bf16x4*>(t + at(r, 4 * u + g, 1));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return *reinterpret_cast<const V*>(t + at(r, 4 * u + g));
+    }
+  }
+  // Operand whose contraction runs down the rows, 16 bit: 32u + 8g .. + 7, fp32: 16u + 4g .. + 3, of 16 columns.
+  // 16 bit: the read takes, for every 16 lanes, 4 rows x 16 columns, lane 4 e + p giving the address of row e,
+  // columns 4p..4p+3, and hands lane i column i of the four rows.
+  // y: the columns 4p..4p+3 are half h of block b0 + p; z: the 16 columns from block b0 on.
+  __device__ __forceinline__ static V col(const char* t, int u, int g, int i, int b0, int h) {
     if constexpr (F32) {
       f32x4 v;
 #pragma unroll
@@ -91,31 +120,27 @@ struct LinTile {
         v[e] = *reinterpret_cast<const float*>(t + at(16 * u + 4 * g + e, b0 + (i >> 2)) + 4 * (i & 3));
       return v;
     } else {
-      // the read takes, for every 16 lanes, 4 rows x 16 columns, lane 4 e + p giving the address of row e, columns
-      // 4p..4p+3, and hands lane i column i of the four rows
-      const int r = 32 * u + 8 * g + (i >> 2);
-      const int p = i & 3;
-      const int b = bs ? b0 + p * bs : b0 + (p >> 1);
-      const int off = bs ? 8 * h : 8 * (p & 1);
+      const int r = 32 * u + 8 * g + (i >> 2), p = i & 3;
+      const int b = USE == kBoth ? b0 + p : b0 + (p >> 1), half = USE == kBoth ? h : p & 1;
       typedef __attribute__((address_space(3))) bf16x4 lds4;
-      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r, b) + off));
-      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r + 4, b) + off));
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r, b, half)));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r + 4, b, half)));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
 };
 
 // A chunk's rows of one tensor on their way from HBM to LDS: 16 bytes a thread and pass, NTH threads.
-template <bool F32, int W, int WP, int NTH>
+template <bool F32, int W, int WP, LinUse USE, int NTH>
 struct LinFetch {
   using Op = LinOp<F32>;
-  using Tile = LinTile<F32, WP>;
+  using Tile = LinTile<F32, WP, USE>;
   static constexpr int NB = W * Op::ES / 16;              // blocks a row in memory
   static constexpr int TOTAL = NB * Op::C;
   static constexpr int NP = (TOTAL + NTH - 1) / NTH;
   static constexpr int RP = NTH / NB;                     // rows a pass
   static_assert(NTH % NB == 0, "a pass takes whole rows");
-  uint4 v[NP];
+  using Data = uint4[NP];
   const char* next;      // this thread's address in the chunk that is fetched next, pass 0
   int64_t step;          // bytes from row to row of the walk
   int row, tid;
@@ -127,7 +152,7 @@ struct LinFetch {
     next = head + tok0 * row_bytes + (pos0 + row) * step + (t % NB) * 16;
   }
   // the next chunk's rows, `valid` of them in the sequence; rows past them repeat the last
-  __device__ __forceinline__ void load(int valid) {
+  __device__ __forceinline__ void load(Data& v, int valid) {
     if (valid >= Op::C) {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
@@ -140,7 +165,7 @@ struct LinFetch {
     next += Op::C * step;
   }
   // rows past `valid` are zeros
-  __device__ __forceinline__ void store(char* tile, int valid) {
+  __device__ __forceinline__ void store(Data& v, char* tile, int valid) {
     if (valid < Op::C) {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
@@ -149,10 +174,10 @@ struct LinFetch {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
       if (TOTAL % NTH == 0 || row + p * RP < Op::C)
-        *reinterpret_cast<uint4*>(tile + Tile::at(row + p * RP, tid % NB)) = v[p];
+        Tile::put(tile, row + p * RP, tid % NB, v[p]);
   }
   // any element of the valid rows is an infinity or NaN (after store)
-  __device__ __forceinline__ bool non_finite() const {
+  __device__ __forceinline__ bool non_finite(const Data& v) const {
     uint32_t odd = 0;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
@@ -275,23 +300,31 @@ struct LinLoader {
   using Op = LinOp<F32>;
   using V = typename Op::V;
   static constexpr int C = Op::C, UK = Sh::AP / Op::KU, TT = C / 16;
-  using TX = LinTile<F32, Sh::AP>;
-  using TP = LinTile<F32, C>;
-  LinFetch<F32, A, Sh::AP, 64 * kLinLoad> fx, fy;
-  LinFetch<F32, Sh::CW, Sh::CW, 64 * kLinLoad> fz;
+  using TX = LinTile<F32, Sh::AP, kRows>;
+  using TY = LinTile<F32, Sh::AP, kBoth>;
+  using TP = LinTile<F32, C, kRows>;
+  LinFetch<F32, A, Sh::AP, kRows, 64 * kLinLoad> fx;
+  LinFetch<F32, A, Sh::AP, kBoth, 64 * kLinLoad> fy;
+  LinFetch<F32, Sh::CW, Sh::CW, kCols, 64 * kLinLoad> fz;
   float pd[4], pm[4], g16;
 
-  __device__ __forceinline__ void load(int valid) {
-    if constexpr (!STATE) fx.load(valid);
-    fy.load(valid);
-    fz.load(valid);
+  // a chunk's rows in registers; two of these are on their way at a time
+  struct Rows {
+    typename decltype(fx)::Data x, y;
+    typename decltype(fz)::Data z;
+  };
+
+  __device__ __forceinline__ void load(Rows& r, int valid) {
+    if constexpr (!STATE) fx.load(r.x, valid);
+    fy.load(r.y, valid);
+    fz.load(r.z, valid);
   }
-  __device__ __forceinline__ void store(char* buf, int* flags, int w, int valid) {
-    fy.store(buf, valid);
-    fz.store(buf + Sh::kXY, valid);
+  __device__ __forceinline__ void store(Rows& r, char* buf, int* flags, int w, int valid) {
+    fy.store(r.y, buf, valid);
+    fz.store(r.z, buf + Sh::kXY, valid);
     if constexpr (!STATE) {
-      fx.store(buf + Sh::kBuf, valid);
-      const bool odd = __any(fz.non_finite());
+      fx.store(r.x, buf + Sh::kBuf, valid);
+      const bool odd = __any(fz.non_finite(r.z));
       if (lane_id() == 0) flags[w] = odd;
     }
   }
@@ -313,14 +346,21 @@ struct LinLoader {
   __device__ __forceinline__ void scores(const char* buf, char* tp, int w, int g, int i) {
     const char* const ty = buf;
     const char* const tx = buf + Sh::kBuf;
+    int strip = -1;
+    V xv[UK];
 #pragma unroll
     for (int n = 0; n < (TT == 4 ? 3 : 1); ++n) {
       int ts, jt;
       if (!tile(w, n, ts, jt)) break;
+      if (ts != strip) {
+#pragma unroll
+        for (int u = 0; u < UK; ++u) xv[u] = TX::row(tx, 16 * ts + i, u, g);
+        strip = ts;
+      }
       f32x4 p = zero4(), p2 = zero4();  // two sums side by side: half the wait for one another
 #pragma unroll
       for (int u = 0; u < UK; ++u)
-        lin_mma((u & 1) ? p2 : p, TX::row(ty, 16 * jt + i, u, g), TX::row(tx, 16 * ts + i, u, g));
+        lin_mma((u & 1) ? p2 : p, TY::row(ty, 16 * jt + i, u, g), xv[u]);
       if (ts == jt) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) p[r] = i >= 4 * g + r ? (p[r] + p2[r]) * pd[r] : 0.f;
@@ -356,7 +396,7 @@ struct LinLoader {
 //
 // The first NW waves hold the state, the other kLinLoad work ahead of them: in the step in which the state's waves take
 // chunk s, they form the scores of chunk s + 1 (which do not depend on the state), write chunk s + 2 to LDS and send
-// for chunk s + 3, with one barrier a step. (STATE: no scores, chunk s + 1 to LDS, s + 2 sent for.)
+// for chunk s + 4, with one barrier a step. (STATE: no scores, chunk s + 1 to LDS, s + 3 sent for.)
 template <int A, int NW, int NT, bool F32, bool STATE, int SPLIT>
 __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
   using Sh = LinShape<A, NW, NT, F32>;
@@ -365,9 +405,10 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   constexpr int C = Op::C, KU = Op::KU, ES = Op::ES, AP = Sh::AP, CW = Sh::CW;
   constexpr int RT = AP / 16, UK = AP / KU, UC = C / KU, TT = C / 16, EZ = F32 ? 4 : 8;
   constexpr int BUF = STATE ? Sh::kBuf : Sh::kBufX;
-  using TX = LinTile<F32, AP>;
-  using TZ = LinTile<F32, CW>;
-  using TP = LinTile<F32, C>;
+  using TX = LinTile<F32, AP, kRows>;
+  using TY = LinTile<F32, AP, kBoth>;
+  using TZ = LinTile<F32, CW, kCols>;
+  using TP = LinTile<F32, C, kRows>;
 
   extern __shared__ char lds[];  // a buffer: y, z, x
   char* const scores = lds + 3 * BUF;  // scores, then (16 bit) what their first bf16 term leaves
@@ -392,8 +433,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     constexpr int tiles = STATE ? 2 : 6;
     for (int id = threadIdx.x; id < tiles * C * 2; id += Sh::kThreads) {
       const int row = (id >> 1) & (C - 1), b = 2 + (id & 1), tile = id / (2 * C);
-      char* const at = STATE ? lds + tile * BUF : lds + (tile >> 1) * BUF + (tile & 1) * Sh::kBuf;
-      *reinterpret_cast<uint4*>(at + TX::at(row, b)) = make_uint4(0, 0, 0, 0);
+      const bool x = !STATE && (tile & 1);
+      char* const at = STATE ? lds + tile * BUF : lds + (tile >> 1) * BUF + (x ? Sh::kBuf : 0);
+      *reinterpret_cast<uint4*>(at + (x ? TX::at(row, b) : TY::at(row, b))) = make_uint4(0, 0, 0, 0);
     }
   }
 
@@ -408,7 +450,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     ld.fz.begin(static_cast<const char*>(sw.z) + ((int64_t)(t.h / sw.zdiv) * E + cg * CW) * ES, rbz, t.tok0, dir,
                 t.pos0, tid);
     auto valid = [&](int s) { return min(C, t.pos1 - (t.pos0 + s * C)); };
-    ld.load(valid(0));
+    typename decltype(ld)::Rows r0, r1;
+    ld.load(r0, valid(0));
+    if (steps > 1) ld.load(r1, valid(1));
     if constexpr (!STATE) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {  // token i of its tile against token 4g + r of the same tile, of the one before
@@ -418,29 +462,37 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       }
       ld.g16 = decay_pow(l2, 16);
     }
-    ld.store(lds, flags, lw, valid(0));
-    if (steps > 1) ld.load(valid(1));
+    ld.store(r0, lds, flags, lw, valid(0));
+    if (steps > 2) ld.load(r0, valid(2));
     if constexpr (STATE) {
       __syncthreads();
-      for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps) ld.store(lds + ((s + 1) & 1) * BUF, flags, lw, valid(s + 1));
-        if (s + 2 < steps) ld.load(valid(s + 2));
+      auto step = [&](int s, typename decltype(ld)::Rows& r) {
+        if (s + 1 < steps) ld.store(r, lds + ((s + 1) & 1) * BUF, flags, lw, valid(s + 1));
+        if (s + 3 < steps) ld.load(r, valid(s + 3));
         __syncthreads();
+      };
+      for (int s = 0; s < steps; s += 2) {
+        step(s, r1);
+        if (s + 1 < steps) step(s + 1, r0);
       }
     } else {
-      if (steps > 1) ld.store(lds + BUF, flags + kLinLoad, lw, valid(1));
-      if (steps > 2) ld.load(valid(2));
+      if (steps > 1) ld.store(r1, lds + BUF, flags + kLinLoad, lw, valid(1));
+      if (steps > 3) ld.load(r1, valid(3));
       __syncthreads();
       ld.scores(lds, scores, lw, g, i);
       __syncthreads();
       int next = 1, after = 2;  // buffers of chunks s + 1, s + 2
-      for (int s = 0; s < steps; ++s) {
+      auto step = [&](int s, typename decltype(ld)::Rows& r) {
         if (s + 1 < steps) ld.scores(lds + next * BUF, scores + ((s + 1) & 1) * Sh::kScores, lw, g, i);
-        if (s + 2 < steps) ld.store(lds + after * BUF, flags + after * kLinLoad, lw, valid(s + 2));
-        if (s + 3 < steps) ld.load(valid(s + 3));
+        if (s + 2 < steps) ld.store(r, lds + after * BUF, flags + after * kLinLoad, lw, valid(s + 2));
+        if (s + 4 < steps) ld.load(r, valid(s + 4));
         next = after;
         after = after == 2 ? 0 : after + 1;
         __syncthreads();
+      };
+      for (int s = 0; s < steps; s += 2) {
+        step(s, r0);
+        if (s + 1 < steps) step(s + 1, r1);
       }
     }
     return;
@@ -507,6 +559,12 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
   // Operands are read from LDS a stage ahead of their products, which the fences keep apart.
 #define GDN2_LIN_FENCE __builtin_amdgcn_sched_barrier(0)
+  // in turn one matrix product and V vector instructions, N times: they run side by side
+#define GDN2_LIN_MIX(N, V)                                 \
+  _Pragma("unroll") for (int mix = 0; mix < (N); ++mix) {  \
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);       \
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);       \
+  }
   V zv[UC][NT];  // this wave's columns of z, contraction over tokens
   V xv[TT];      // rows of x, unit 0
   auto fetch = [&](const char* buf) {
@@ -514,7 +572,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     for (int u = 0; u < UC; ++u)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        zv[u][n] = TZ::col(buf + Sh::kXY, u, g, i, F32 ? c0 / 4 + 4 * n : c0 / 8 + 2 * n, 0, 0);
+        zv[u][n] = TZ::col(buf + Sh::kXY, u, g, i, F32 ? c0 / 4 + 4 * n : c0 / 8 + 2 * n, 0);
     if constexpr (!STATE) {
 #pragma unroll
       for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
@@ -523,7 +581,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   constexpr int MP = RT >= 2 ? 2 : 1, NS = UC * RT / MP;  // tiles a stage of the update, its stages
   auto y_of = [&](const char* ty, int st, int m) {        // operand of stage st, its tile m
     const int u = st / (RT / MP), mt = st % (RT / MP) * MP + m;
-    return F32 ? TX::col(ty, u, g, i, 4 * mt, 0, 0) : TX::col(ty, u, g, i, 4 * (mt >> 1), 1, mt & 1);
+    return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);
   };
   __syncthreads();
   if constexpr (!STATE) __syncthreads();
@@ -556,12 +614,29 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
             }
       };
       const int4 odd4 = *reinterpret_cast<const int4*>(flags + (now == 0 ? 2 : now - 1) * kLinLoad);
-      // r^T from the state: rows are columns of the state, columns are tokens
-      f32x4 R[TT][NT];
+      // r^T from the state and from the scores: rows are columns of the state, columns are tokens
+      f32x4 R[TT][NT], R2[TT][NT];
 #pragma unroll
       for (int k = 0; k < TT; ++k)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) R[k][n] = zero4();
+        for (int n = 0; n < NT; ++n) R[k][n] = R2[k][n] = zero4();
+      V zh[2][NT], zl[2][NT];
+      auto state_operand = [&](int u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (F32) {
+            zh[u & 1][n] = Z[u][n];
+          } else {
+            float x[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][n][r], x[4 + r] = Z[2 * u + 1][n][r];
+            zh[u & 1][n] = pack_hi(x);
+            sub_hi(x);
+            zl[u & 1][n] = pack_rne(x);
+          }
+        }
+      };
+      state_operand(0);
 #pragma unroll
       for (int u = 0; u < UK; ++u) {
         V xn[TT];
@@ -572,30 +647,19 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
           get_scores(0, H1);
         }
         GDN2_LIN_FENCE;
-        V zh[NT];
-        V zl[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if constexpr (F32) {
-            zh[n] = Z[u][n];
-          } else {
-            float x[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][n][r], x[4 + r] = Z[2 * u + 1][n][r];
-            zh[n] = pack_hi(x);
-            sub_hi(x);
-            zl[n] = pack_rne(x);
-          }
-        }
 #pragma unroll
         for (int k = 0; k < TT; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zh[n], xv[k]);
+          for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zh[u & 1][n], xv[k]);
         if constexpr (!F32) {
 #pragma unroll
           for (int k = 0; k < TT; ++k)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zl[n], xv[k]);
+            for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zl[u & 1][n], xv[k]);
+        }
+        if (u + 1 < UK) {
+          state_operand(u + 1);  // beside the products
+          GDN2_LIN_MIX((F32 ? 1 : 2) * TT * NT, 4);
         }
         GDN2_LIN_FENCE;
         if (u + 1 < UK) {
@@ -620,12 +684,6 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       }
       get_scores(H1, NU);
       GDN2_LIN_FENCE;
-#pragma unroll
-      for (int k = 0; k < TT; ++k)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) R[k][n][r] *= ro[k];
       auto add_scores = [&](int from, int to) {
         int n = 0;
 #pragma unroll
@@ -635,8 +693,8 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
             if (n >= from && n < to) {
 #pragma unroll
               for (int c = 0; c < NT; ++c) {
-                if constexpr (!F32) lin_mma(R[k][c], zp[u][c], pl[n]);
-                lin_mma(R[k][c], zp[u][c], ph[n]);
+                if constexpr (!F32) lin_mma(R2[k][c], zp[u][c], pl[n]);
+                lin_mma(R2[k][c], zp[u][c], ph[n]);
               }
             }
       };
@@ -668,7 +726,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
               for (int r = 0; r < 4; ++r) {
                 const int c = c0 + 16 * n + 4 * g + r;
                 const float z = load1<F32>(tz + TZ::at(j, c * ES / 16), c % (16 / ES));
-                if (j <= 16 * k + i && !(fabsf(z) <= 3.4028235e38f)) R[k][n][r] += p * z;
+                if (j <= 16 * k + i && !(fabsf(z) <= 3.4028235e38f)) R2[k][n][r] += p * z;
               }
             }
       }
@@ -678,7 +736,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const int64_t at = rat + 16 * k * rstep + 16 * n;
-            const f32x4 x = R[k][n];
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = fmaf(R[k][n][r], ro[k], R2[k][n][r]);
             if (F32 || sw.r_f32) st4(static_cast<float*>(sw.r) + at, x[0], x[1], x[2], x[3]);
             else st4(static_cast<__bf16*>(sw.r) + at, x[0], x[1], x[2], x[3]);
           }
@@ -708,7 +768,38 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
             for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], rest, Z[m][n][r]);
       }
       // Z <- g^n Z + sum_j y_j (c_j z_j)^T. 16 bit: c_j z_j in SPLIT terms
-      V zs[F32 ? 1 : SPLIT][NT];
+      constexpr int TERMS = F32 ? 1 : SPLIT;
+      V zs[2][TERMS][NT];
+      auto terms = [&](int u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (F32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zs[u & 1][0][n][e] = cz[u][e] * zv[u][n][e];
+          } else {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
+#pragma unroll
+            for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
+              zs[u & 1][t2][n] = pack_hi(x);
+              sub_hi(x);
+            }
+            zs[u & 1][SPLIT - 1][n] = pack_rne(x);
+          }
+        }
+      };
+      auto decay = [&](int m0) {
+#pragma unroll
+        for (int m = 0; m < MP; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) Z[m0 + m][n][r] *= gC;
+      };
+      constexpr int SU = RT / MP;  // stages a unit
+      terms(0);
+      decay(0);
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
         if (st + 2 < NS) {
@@ -716,40 +807,17 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
           for (int m = 0; m < MP; ++m) y[(st + 2) % 3][m] = y_of(ty, st + 2, m);
         }
         GDN2_LIN_FENCE;
-        const int u = st / (RT / MP), m0 = st % (RT / MP) * MP;
-        if (m0 == 0) {
+        const int u = st / SU, m0 = st % SU * MP;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if constexpr (F32) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) zs[0][n][e] = cz[u][e] * zv[u][n][e];
-            } else {
-              float x[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
-#pragma unroll
-              for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
-                zs[t2][n] = pack_hi(x);
-                sub_hi(x);
-              }
-              zs[SPLIT - 1][n] = pack_rne(x);
-            }
-          }
-        }
-        if (u == 0) {
+        for (int t2 = TERMS - 1; t2 >= 0; --t2)
 #pragma unroll
           for (int m = 0; m < MP; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) Z[m0 + m][n][r] *= gC;
-        }
-#pragma unroll
-        for (int t2 = (F32 ? 1 : SPLIT) - 1; t2 >= 0; --t2)
-#pragma unroll
-          for (int m = 0; m < MP; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) lin_mma(Z[m0 + m][n], y[st % 3][m], zs[t2][n]);
+            for (int n = 0; n < NT; ++n) lin_mma(Z[m0 + m][n], y[st % 3][m], zs[u & 1][t2][n]);
+        // beside the products: the next stage's decay, the next unit's terms
+        if (st + 1 < SU) decay(m0 + MP);
+        if (st % SU == SU - 1 && u + 1 < UC) terms(u + 1);
+        GDN2_LIN_MIX(TERMS * MP * NT, 4);
         GDN2_LIN_FENCE;
       }
     }
@@ -762,6 +830,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     }
   }
 #undef GDN2_LIN_FENCE
+#undef GDN2_LIN_MIX
 
   if (want_last) {
     float* dst = STATE ? a.seg_state + ((int64_t)(a.cu ? t.slot + 1 : t.slot + a.N) * a.H + t.h) * A * E
