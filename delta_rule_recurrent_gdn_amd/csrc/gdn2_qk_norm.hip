@@ -89,28 +89,49 @@ struct Turn {
       }
     }
   }
-  // x <- R x, or R^T x (BACK)
+  // x <- R x, or R^T x (BACK); o: the partner lane's channels (halves)
   template <bool BACK>
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
+  __device__ __forceinline__ void turn(float (&x)[8], const float (&o)[8]) const {
+    if (!on) return;
     if constexpr (PAIRS) {
-      if (on) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float u = x[2 * e], v = x[2 * e + 1], s = BACK ? -sn[e] : sn[e];
-          x[2 * e] = u * cs[e] - v * s;
-          x[2 * e + 1] = v * cs[e] + u * s;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[2 * e], v = x[2 * e + 1], s = BACK ? -sn[e] : sn[e];
+        x[2 * e] = u * cs[e] - v * s;
+        x[2 * e + 1] = v * cs[e] + u * s;
       }
     } else {
-      float o[8];
+      const bool minus = second == BACK;  // the first channels take -sin, the second +sin; R^T the other way
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[e] + (minus ? -o[e] : o[e]) * sn[e];
+    }
+  }
+  __device__ __forceinline__ void forward(float (&x)[8]) const {
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = PAIRS ? 0.f : __shfl(x[e], partner);
+    turn<false>(x, o);
+  }
+  // R^T of a row still as it is in memory: its partner's channels travel packed
+  template <bool F32>
+  __device__ __forceinline__ void back(const Raw8<F32>& r, float (&x)[8]) const {
+    cvt(r, x);
+    float o[8];
+    if constexpr (PAIRS) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    } else if constexpr (F32) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = __shfl(x[e], partner);
-      if (on) {
-        const bool minus = second == BACK;  // the first channels take -sin, the second +sin; R^T the other way
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[e] + (minus ? -o[e] : o[e]) * sn[e];
-      }
+    } else {
+      Raw8<false> p;
+      p.u.x = __shfl((int)r.u.x, partner);
+      p.u.y = __shfl((int)r.u.y, partner);
+      p.u.z = __shfl((int)r.u.z, partner);
+      p.u.w = __shfl((int)r.u.w, partner);
+      cvt(p, o);
     }
+    turn<true>(x, o);
   }
 };
 
@@ -165,7 +186,7 @@ __global__ __launch_bounds__(64 * kWaves) void gdn2_qk_norm_fwd_kernel(QkNormArg
         const float r = 1.f / sqrtf(fmaf(group_sum<LPR>(q), a.inv_count, a.eps));
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[u][e] = x[u][e] * r * w[e];
-        turn.template apply<false>(x[u]);
+        turn.forward(x[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -179,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaves) void gdn2_qk_norm_fwd_kernel(QkNormArg
 // Tokens go round the workgroups, so that a wave's sums of the weights' gradients stay in its registers; the
 // workgroups' sums are added in a second kernel, in a fixed order.
 template <int D, bool F32, bool F32DY, bool PAIRS>
-__global__ __launch_bounds__(64 * kWaves) void gdn2_qk_norm_bwd_kernel(QkNormArgs a, int split) {
+__global__ __launch_bounds__(64 * kWaves, 4) void gdn2_qk_norm_bwd_kernel(QkNormArgs a, int split) {
   constexpr int LPR = D / 8, RW = 64 / LPR;
   __shared__ float tables[kWaves][128];
   __shared__ float sums[kWaves][2][D];
@@ -205,39 +226,39 @@ __global__ __launch_bounds__(64 * kWaves) void gdn2_qk_norm_bwd_kernel(QkNormArg
     for (int side = 0; side < 2; ++side) {
       const QkNormSide& s = a.s[side];
       const int j0 = side == 0 ? i0 : max(i0, st.q) - st.q, j1 = side == 0 ? min(i1, st.q) : i1 - st.q;
-      constexpr int U = 2;  // rows in flight
+      constexpr int U = F32 || F32DY ? 2 : 4;  // rows in flight, as they are in memory
       for (int j = j0; j < j1; j += U) {
-        float x[U][8], d[U][8];
+        Raw8<F32> xr[U];
+        Raw8<F32DY> dr[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int head = min(min(j + u, j1 - 1) * RW + row, s.heads - 1);
-          load8<F32>(s.x, n * s.x_stride + (int64_t)head * D + 8 * c, x[u]);
-          load8<F32DY>(s.dy, (n * s.heads + head) * D + 8 * c, d[u]);
+          ld_raw(xr[u], s.x, n * s.x_stride + (int64_t)head * D + 8 * c);
+          ld_raw(dr[u], s.dy, (n * s.heads + head) * D + 8 * c);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const bool ok = j + u < j1 && (j + u) * RW + row < s.heads;
-          turn.template apply<true>(d[u]);
+          if (j + u >= j1) break;
+          const int head = (j + u) * RW + row;
+          const bool ok = head < s.heads;
+          float x[8], d[8];
+          turn.back(dr[u], d);
+          cvt(xr[u], x);
           float q = 0.f, p = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            d[u][e] *= s.scale;
-            q = fmaf(x[u][e], x[u][e], q);
-            p = fmaf(x[u][e], d[u][e] * w[side][e], p);
+            d[e] *= s.scale;
+            q = fmaf(x[e], x[e], q);
+            p = fmaf(x[e], d[e] * w[side][e], p);
           }
           const float r = 1.f / sqrtf(fmaf(group_sum<LPR>(q), a.inv_count, a.eps));
           const float t = group_sum<LPR>(p) * a.inv_count * r * r;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float u_ = d[u][e];
-            if (ok) dw[side][e] = fmaf(u_ * x[u][e], r, dw[side][e]);
-            x[u][e] = r * (u_ * w[side][e] - x[u][e] * t);
+            if (ok) dw[side][e] = fmaf(d[e] * x[e], r, dw[side][e]);
+            x[e] = r * (d[e] * w[side][e] - x[e] * t);
           }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int head = (j + u) * RW + row;
-          if (j + u < j1 && head < s.heads) store8<F32>(s.y, n * s.y_stride + (int64_t)head * D + 8 * c, x[u]);
+          if (ok) store8<F32>(s.y, n * s.y_stride + (int64_t)head * D + 8 * c, x);
         }
       }
     }

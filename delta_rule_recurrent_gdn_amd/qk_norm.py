@@ -9,7 +9,7 @@ fused projection: their heads lie side by side, and the rows (all leading dimens
 import torch
 
 from . import _lib
-from .linattn import _code, _like, _on, _ptr, _scratch
+from .linattn import _code, _like, _on, _ptr, _scratch, _stream
 
 
 def _rows(name, t, like=None):
@@ -98,7 +98,7 @@ def gdn2_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, q_weight=None, k_
     dt, dev, rows, period, Hq, Hk, D, rot, sq, sk = _common(q, k, positions, inv_freq, q_weight, k_weight)
     q_out, so = _output("q_out", q_out, q)
     k_out, sko = _output("k_out", k_out, k)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream(dev)
     with _on(dev):
         st = lib.gdn2_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
                                        _ptr(inv_freq), _ptr(q_out), _ptr(k_out), rows, period, Hq, Hk, D, rot, sq, sk,
@@ -127,7 +127,7 @@ def gdn2_qk_norm_rope_bwd(dq_out, dk_out, q, k, positions=None, inv_freq=None, q
     if dqw is not None or dkw is not None:
         need = lib.gdn2_qk_norm_rope_workspace_bytes(rows, Hq, Hk, D)
     ws, ws_bytes, keep = _scratch(workspace, need, dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream(dev)
     with _on(dev):
         st = lib.gdn2_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
                                        _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), ws,
