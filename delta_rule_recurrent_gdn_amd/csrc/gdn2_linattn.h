@@ -27,10 +27,14 @@ struct LinSweep {
   const float* Z0;               // entering states [N, H, ...], nullable; element (a, e) at a * z0_rs + e * z0_cs
   int z0_rs, z0_cs;
   float* Z1;                     // last states [N, H, A, E], nullable
+  float* seg_state;              // [max_segs (x N when dense)][H][A][E]: the state entering each piece
 };
 
+constexpr int kLinSweeps = 3;    // sweeps of one launch at most
+
 struct LinArgs {
-  LinSweep sw;
+  LinSweep sw[kLinSweeps];       // of the same A and E, run side by side
+  int sweeps;
   const float* log_decay;        // [H]
   int N, T, H, A, E;             // sequences (batch rows), tokens a row (packed: all of them), heads of the states
   bool f32;
@@ -39,17 +43,16 @@ struct LinArgs {
   bool pieces;
   int seg_tok;
   int max_segs;                  // dense: pieces of a sequence; packed: bound of all sequences' pieces
-  float* seg_state;              // [max_segs (x N when dense)][H][A][E]: the state entering that piece
   // packed batches: offsets and piece tables on the device (null: dense)
   const int64_t* cu;
   const int* seg_first;
   const int* seg_seq;
 };
 
-int linattn_seg_tokens(int N, int T, int H, int A, int E, bool packed);
+int linattn_seg_tokens(int N, int T, int H, int E, int sweeps, bool packed, bool f32);
 int linattn_max_segs(int N, int T, int seg_tok, bool packed);
-// piece states of a sweep, joined and handed to the sweep's pieces, then the sweep itself
-hipError_t launch_linattn_sweep(const LinArgs& a, hipStream_t s);
+// piece states of the sweeps, joined and handed to the sweeps' pieces, then the sweeps themselves
+hipError_t launch_linattn_sweeps(const LinArgs& a, hipStream_t s);
 // dst[row, j, :] = sum over i < G of src[row, j G + i, :] (src fp32), rounded to the type of dst; packed
 // batches (cu [N + 1]): for rows cu[0] .. cu[N] - 1 alone
 hipError_t launch_linattn_group_sum(const float* src, void* dst, int64_t rows, int heads, int G, int D, bool f32,

@@ -22,6 +22,7 @@ constexpr int kJoinThreads = 256;
 
 // One thread an element quadruple of a (sequence, head)'s state.
 __global__ __launch_bounds__(kJoinThreads) void gdn2_linattn_join_kernel(LinArgs a, int blocks) {
+  const LinSweep& sw = a.sw[blockIdx.y];
   const int chain = blockIdx.x / blocks;
   const int n = chain / a.H, h = chain - n * a.H;
   const int at = ((blockIdx.x % blocks) * kJoinThreads + threadIdx.x) * 4;
@@ -39,20 +40,20 @@ __global__ __launch_bounds__(kJoinThreads) void gdn2_linattn_join_kernel(LinArgs
   }
   const int64_t state = (int64_t)a.A * a.E;
   float z[4] = {0.f, 0.f, 0.f, 0.f};
-  if (a.sw.Z0) {
-    const float* src = a.sw.Z0 + (int64_t)chain * state;
+  if (sw.Z0) {
+    const float* src = sw.Z0 + (int64_t)chain * state;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = src[(int64_t)row * a.sw.z0_rs + (int64_t)(col + e) * a.sw.z0_cs];
+    for (int e = 0; e < 4; ++e) z[e] = src[(int64_t)row * sw.z0_rs + (int64_t)(col + e) * sw.z0_cs];
   }
   if (nseg == 0) {  // a sequence without tokens: its last state is its first
-    if (a.sw.Z1) *reinterpret_cast<float4*>(a.sw.Z1 + (int64_t)chain * state + at) = make_float4(z[0], z[1], z[2], z[3]);
+    if (sw.Z1) *reinterpret_cast<float4*>(sw.Z1 + (int64_t)chain * state + at) = make_float4(z[0], z[1], z[2], z[3]);
     return;
   }
   if (!a.pieces) return;
   const float ld = a.log_decay[h];
   const double d = exp((ld < -1e4f ? -1e4 : (double)ld) * a.seg_tok);
   const float hi = (float)d, lo = (float)(d - hi);
-  float4* p = reinterpret_cast<float4*>(a.seg_state + ((int64_t)slot * a.H + h) * state + at);
+  float4* p = reinterpret_cast<float4*>(sw.seg_state + ((int64_t)slot * a.H + h) * state + at);
   const int64_t stride = (int64_t)step * a.H * state / 4;
   p[0] = make_float4(z[0], z[1], z[2], z[3]);
   float4 next = nseg > 1 ? p[stride] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -90,37 +91,42 @@ __global__ __launch_bounds__(256) void gdn2_linattn_group_sum_kernel(const float
 
 }  // namespace
 
-int linattn_seg_tokens(int N, int T, int H, int A, int E, bool packed) {
-  (void)A;
-  constexpr int kChunk = 64, kLeast = 8, kWorkgroups = 512;
-  const int64_t chunks = (T + kChunk - 1) / kChunk;
-  const int64_t wide = (int64_t)H * ((E + 63) / 64);  // workgroups a piece
+// Tokens a piece: as many pieces as give every CU its one workgroup (the sweeps' LDS holds one), of at least four
+// chunks (fewer cost more in states written, joined and read than the shorter walk saves: 2 x 2055 tokens of 12
+// heads, backward, 115 us with four chunks a piece, 137 with two, 118 with eight; fp32, 2 x 1001 of 8 heads, whose
+// chunks are half as long: 27 us with four, 36 with eight, 56 with sixteen).
+int linattn_seg_tokens(int N, int T, int H, int E, int sweeps, bool packed, bool f32) {
+  constexpr int kUnit = 64, kWorkgroups = 256;
+  const int64_t units = (T + kUnit - 1) / kUnit, least = f32 ? 2 : 4;
+  const int64_t wide = (int64_t)H * ((E + 63) / 64) * sweeps;  // workgroups a piece
   int64_t L;
   if (packed) {
-    L = (chunks * wide + kWorkgroups - 1) / kWorkgroups;
+    L = (units * wide + kWorkgroups - 1) / kWorkgroups;
   } else {
-    const int64_t pieces = N * wide >= 256 ? 1 : (kWorkgroups + N * wide - 1) / (N * wide);
-    L = (chunks + pieces - 1) / pieces;
+    const int64_t pieces = N * wide >= kWorkgroups ? 1 : (kWorkgroups + N * wide - 1) / (N * wide);
+    L = (units + pieces - 1) / pieces;
   }
-  if (L < kLeast) L = kLeast;
-  if (L > chunks) L = chunks;
-  return (int)(L * kChunk);
+  if (L < least) L = least;
+  if (L > units) L = units;
+  return (int)(L * kUnit);
 }
 
 int linattn_max_segs(int N, int T, int seg_tok, bool packed) {
   return packed ? T / seg_tok + N : (T + seg_tok - 1) / seg_tok;
 }
 
-hipError_t launch_linattn_sweep(const LinArgs& a, hipStream_t s) {
+hipError_t launch_linattn_sweeps(const LinArgs& a, hipStream_t s) {
   const auto run = a.f32 ? launch_linattn_f32 : launch_linattn_bf16;
   if (a.pieces) {
     const hipError_t e = run(a, true, s);
     if (e != hipSuccess) return e;
   }
-  if (a.pieces || (a.cu && a.sw.Z1)) {
+  bool last = false;
+  for (int i = 0; i < a.sweeps; ++i) last |= a.sw[i].Z1 != nullptr;
+  if (a.pieces || (a.cu && last)) {
     const int blocks = (a.A * a.E / 4 + kJoinThreads - 1) / kJoinThreads;
-    hipLaunchKernelGGL(gdn2_linattn_join_kernel, dim3((unsigned)(a.N * a.H * blocks)), dim3(kJoinThreads), 0, s, a,
-                       blocks);
+    hipLaunchKernelGGL(gdn2_linattn_join_kernel, dim3((unsigned)(a.N * a.H * blocks), a.sweeps), dim3(kJoinThreads), 0,
+                       s, a, blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

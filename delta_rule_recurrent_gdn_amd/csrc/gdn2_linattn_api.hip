@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <initializer_list>
+#include <utility>
 
 #include "gdn2.h"
 #include "gdn2_linattn.h"
@@ -37,26 +38,29 @@ int check_sizes(int N, int T, int Hk, int H, int Dk, int Dv, int dt) {
 }
 
 // Sizes of a call: the pieces its sequences are cut into, and its workspace
-// [tables of a packed batch][piece states][fp32 gradients of shared heads].
+// [tables of a packed batch][piece states of each sweep][fp32 dq and dk of shared heads].
 struct Plan {
   int seg_tok, max_segs;
   bool pieces;
-  size_t states, partial, need;  // offsets of the last two, and the end
-  bool fits;                     // every launch within the grid's limits
+  size_t states, state_bytes, partial, partial_bytes, need;  // offsets, and sizes of one
+  bool fits;                                                 // every launch within the grid's limits
 };
 
-Plan plan(bool bwd, int N, int T, int Hk, int H, int Dk, int Dv, bool packed) {
+Plan plan(bool bwd, int N, int T, int Hk, int H, int Dk, int Dv, bool packed, int dt) {
   Plan p{};
+  const int sweeps = bwd ? 3 : 1;
   const int E = bwd && Dk < Dv ? Dk : Dv;  // the sweeps' columns (the backward's: Dk and Dv)
-  p.seg_tok = gdn2::linattn_seg_tokens(N, T, H, Dk, E, packed);
+  p.seg_tok = gdn2::linattn_seg_tokens(N, T, H, E, bwd ? 2 : 1, packed, dt == GDN2_F32);
   p.max_segs = gdn2::linattn_max_segs(N, T, p.seg_tok, packed);
   p.pieces = packed ? p.seg_tok < T : p.max_segs > 1;
   p.states = packed ? al256(gdn2::varlen_table_bytes(N, T, p.seg_tok, 0)) : 0;
   const size_t slots = (size_t)p.max_segs * (packed ? 1 : N);
-  p.partial = p.states + (p.pieces ? al256(slots * H * Dk * Dv * 4) : 0);
-  p.need = p.partial + (bwd && H != Hk ? al256((size_t)(packed ? 1 : N) * T * H * Dk * 4) : 0);
+  p.state_bytes = p.pieces ? al256(slots * H * Dk * Dv * 4) : 0;
+  p.partial = p.states + sweeps * p.state_bytes;
+  p.partial_bytes = bwd && H != Hk ? al256((size_t)(packed ? 1 : N) * T * H * Dk * 4) : 0;
+  p.need = p.partial + 2 * p.partial_bytes;
   const int wide = (Dk > Dv ? Dk : Dv) <= 64 ? 1 : 2;
-  p.fits = slots * H * wide < (size_t)INT_MAX - 64 && (size_t)N * H * 16 < (size_t)INT_MAX;
+  p.fits = slots * H * wide * sweeps < (size_t)INT_MAX - 64 && (size_t)N * H * 16 < (size_t)INT_MAX;
   return p;
 }
 
@@ -75,7 +79,7 @@ struct Call {
 
 // Checks that come after the sizes', and the packed batch's tables. done: nothing (more) to do, return st.
 int begin(const Call& c, bool bwd, Plan& p, gdn2::LinArgs& a) {
-  p = plan(bwd, c.N, c.T, c.Hk, c.H, c.Dk, c.Dv, c.cu != nullptr);
+  p = plan(bwd, c.N, c.T, c.Hk, c.H, c.Dk, c.Dv, c.cu != nullptr, c.dt);
   if (!p.fits) return GDN2_ERR_SHAPE;
   if (p.need > 0) {
     if (c.ws == nullptr || c.ws_bytes < p.need) return GDN2_ERR_WORKSPACE;
@@ -90,7 +94,6 @@ int begin(const Call& c, bool bwd, Plan& p, gdn2::LinArgs& a) {
   a.pieces = p.pieces;
   a.seg_tok = p.seg_tok;
   a.max_segs = p.max_segs;
-  a.seg_state = reinterpret_cast<float*>(c.ws + p.states);
   if (c.cu) {
     gdn2::Varlen vl;
     const hipError_t e = gdn2::launch_varlen_plan(reinterpret_cast<const int64_t*>(c.cu), c.N, c.T, p.seg_tok, 0, c.ws,
@@ -123,8 +126,10 @@ int forward(const Call& c, void* o, float* S_final) {
   const int G = c.H / c.Hk;
   a.A = c.Dk;
   a.E = c.Dv;
-  a.sw = gdn2::LinSweep{c.q, c.k, c.v, o, G, G, 1, false, false, 1, true, 1.f, c.scale, c.S0, c.Dv, 1, S_final};
-  return hip_status(gdn2::launch_linattn_sweep(a, c.stream));
+  a.sw[0] = gdn2::LinSweep{c.q, c.k, c.v, o, G, G, 1, false, false, 1, true, 1.f, c.scale, c.S0, c.Dv, 1, S_final,
+                           reinterpret_cast<float*>(c.ws + p.states)};
+  a.sweeps = 1;
+  return hip_status(gdn2::launch_linattn_sweeps(a, c.stream));
 }
 
 int backward(const Call& c, const void* dO, const float* dS_final, void* dq, void* dk, void* dv, float* dS0) {
@@ -146,28 +151,42 @@ int backward(const Call& c, const void* dO, const float* dS_final, void* dq, voi
   if (st != GDN2_OK) return st;
   const int G = c.H / c.Hk;
   const int64_t rows = c.cu ? c.T : (int64_t)c.N * c.T;
-  float* const partial = reinterpret_cast<float*>(c.ws + p.partial);
-  const auto shared = [&](void* d) {
-    return G == 1 ? hipSuccess
-                  : gdn2::launch_linattn_group_sum(partial, d, rows, c.Hk, G, c.Dk, a.f32, a.cu, c.N, c.stream);
-  };
+  const auto at = [&](size_t offset) { return reinterpret_cast<float*>(c.ws + offset); };
+  void* const dq_to = G == 1 ? dq : at(p.partial);
+  void* const dk_to = G == 1 ? dk : at(p.partial + p.partial_bytes);
   // dq: the forward recurrence of S^T, over (dO, v, k)
+  const gdn2::LinSweep sq{dO, c.v, c.k, dq_to, 1, 1, G, G > 1, false, 1, false, 1.f, c.scale,
+                          c.S0, 1, c.Dv, nullptr, at(p.states)};
+  // dk: the reversed recurrence of the state's gradient, transposed, over (v, dO, q)
+  const gdn2::LinSweep sk{c.v, dO, c.q, dk_to, 1, 1, G, G > 1, true, 0, false, c.scale, 1.f,
+                          dS_final, 1, c.Dv, nullptr, at(p.states + p.state_bytes)};
+  // dv: the same state, over (k, q, dO); its last value is dS0
+  const gdn2::LinSweep sv{c.k, c.q, dO, dv, G, G, 1, false, true, 0, dS0 != nullptr, c.scale, 1.f,
+                          dS_final, c.Dv, 1, dS0, at(p.states + 2 * p.state_bytes)};
+  hipError_t e = hipSuccess;
+  // dS0 may be S0 or dS_final: with pieces all entering states are read before the last are written, else they are
+  // not when dk's and dv's sweeps run side by side
+  const bool apart = dS0 != nullptr && (dS0 == c.S0 || dS0 == dS_final) && !p.pieces;
   a.A = c.Dv;
   a.E = c.Dk;
-  a.sw = gdn2::LinSweep{dO, c.v, c.k, G == 1 ? dq : partial, 1, 1, G, G > 1, false, 1, false, 1.f, c.scale,
-                        c.S0, 1, c.Dv, nullptr};
-  hipError_t e = gdn2::launch_linattn_sweep(a, c.stream);
-  if (e == hipSuccess) e = shared(dq);
-  // dk: the reversed recurrence of the state's gradient, transposed, over (v, dO, q)
-  a.sw = gdn2::LinSweep{c.v, dO, c.q, G == 1 ? dk : partial, 1, 1, G, G > 1, true, 0, false, c.scale, 1.f,
-                        dS_final, 1, c.Dv, nullptr};
-  if (e == hipSuccess) e = gdn2::launch_linattn_sweep(a, c.stream);
-  if (e == hipSuccess) e = shared(dk);
-  // dv: the same state, over (k, q, dO); its last value is dS0
-  a.A = c.Dk;
-  a.E = c.Dv;
-  a.sw = gdn2::LinSweep{c.k, c.q, dO, dv, G, G, 1, false, true, 0, true, c.scale, 1.f, dS_final, c.Dv, 1, dS0};
-  if (e == hipSuccess) e = gdn2::launch_linattn_sweep(a, c.stream);
+  a.sw[0] = sq;
+  a.sw[1] = sk;
+  a.sw[2] = sv;
+  a.sweeps = c.Dk == c.Dv && !apart ? 3 : 2;
+  e = gdn2::launch_linattn_sweeps(a, c.stream);
+  if (e == hipSuccess && a.sweeps == 2) {
+    a.A = c.Dk;
+    a.E = c.Dv;
+    a.sw[0] = sv;
+    a.sweeps = 1;
+    e = gdn2::launch_linattn_sweeps(a, c.stream);
+  }
+  if (G > 1) {
+    for (auto x : {std::pair<void*, void*>{dq_to, dq}, {dk_to, dk}})
+      if (e == hipSuccess)
+        e = gdn2::launch_linattn_group_sum(static_cast<float*>(x.first), x.second, rows, c.Hk, G, c.Dk, a.f32, a.cu,
+                                           c.N, c.stream);
+  }
   return hip_status(e);
 }
 
@@ -225,7 +244,7 @@ extern "C" {
 size_t gdn2_linattn_workspace_bytes(int op, int N, int T, int Hk, int H, int Dk, int Dv, int packed, int dt) {
   if (op != GDN2_OP_FWD && op != GDN2_OP_BWD) return 0;
   if (check_sizes(N, T, Hk, H, Dk, Dv, dt) != GDN2_OK || N == 0 || T == 0 || H == 0) return 0;
-  return plan(op == GDN2_OP_BWD, N, T, Hk, H, Dk, Dv, packed != 0).need;
+  return plan(op == GDN2_OP_BWD, N, T, Hk, H, Dk, Dv, packed != 0, dt).need;
 }
 
 int gdn2_linattn_fwd_chunked(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,

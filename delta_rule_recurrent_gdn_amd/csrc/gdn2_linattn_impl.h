@@ -250,7 +250,7 @@ struct LinTask {
   int len, pos0, pos1;
 };
 
-__device__ __forceinline__ bool lin_task(const LinArgs& a, int item, LinTask& t) {
+__device__ __forceinline__ bool lin_task(const LinArgs& a, int item, bool rev, LinTask& t) {
   // items: head fastest, then sequence (dense), then piece
   t.h = item % a.H;
   int rest = item / a.H;
@@ -273,17 +273,18 @@ __device__ __forceinline__ bool lin_task(const LinArgs& a, int item, LinTask& t)
     begin = (int64_t)t.n * a.T;
     t.len = a.T;
   }
-  t.tok0 = a.sw.rev ? begin + t.len - 1 : begin;
+  t.tok0 = rev ? begin + t.len - 1 : begin;
   t.pos0 = t.seg * a.seg_tok;
   t.pos1 = min(t.len, t.pos0 + a.seg_tok);
   return true;
 }
 
-// Block -> (item, column group): a head's column groups take workgroups 8 apart, so that they run on one XCD and
-// read x and y through its L2 once.
-__device__ __forceinline__ void lin_block(int ncg, int& item, int& cg) {
-  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  item = (slot / ncg) * 8 + xcd;
+// Block -> (item, sweep, column group): a head's column groups and sweeps take workgroups 8 apart, so that they run on
+// one XCD and read what they share through its L2 once.
+__device__ __forceinline__ void lin_block(int ncg, int sweeps, int& item, int& sweep, int& cg) {
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, per = ncg * sweeps;
+  item = (slot / per) * 8 + xcd;
+  sweep = slot % per / ncg;
   cg = slot % ncg;
 }
 
@@ -415,15 +416,15 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   int* const flags = reinterpret_cast<int*>(scores + 2 * Sh::kScores);  // [3][kLinLoad]: z has an infinity or NaN
 
   const int ncg = (a.E + CW - 1) / CW;
-  int item, cg;
-  lin_block(ncg, item, cg);
+  int item, sweep, cg;
+  lin_block(ncg, a.sweeps, item, sweep, cg);
+  const LinSweep& sw = a.sw[sweep];
   LinTask t;
-  if (!lin_task(a, item, t)) return;
+  if (!lin_task(a, item, sw.rev, t)) return;
   if (STATE && t.seg + 1 >= t.nseg) return;
 
   const int l = lane_id(), g = l >> 4, i = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const LinSweep& sw = a.sw;
   const int dir = sw.rev ? -1 : 1;
   const int E = a.E;
   const int steps = (t.pos1 - t.pos0 + C - 1) / C;
@@ -533,7 +534,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     const float* src = nullptr;
     int rs = E, cs = 1;
     if (a.pieces) {
-      src = a.seg_state + ((int64_t)t.slot * a.H + t.h) * A * E;
+      src = sw.seg_state + ((int64_t)t.slot * a.H + t.h) * A * E;
     } else if (sw.Z0) {
       src = sw.Z0 + ((int64_t)t.n * a.H + t.h) * A * E;
       rs = sw.z0_rs;
@@ -833,7 +834,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #undef GDN2_LIN_MIX
 
   if (want_last) {
-    float* dst = STATE ? a.seg_state + ((int64_t)(a.cu ? t.slot + 1 : t.slot + a.N) * a.H + t.h) * A * E
+    float* dst = STATE ? sw.seg_state + ((int64_t)(a.cu ? t.slot + 1 : t.slot + a.N) * a.H + t.h) * A * E
                        : sw.Z1 + ((int64_t)t.n * a.H + t.h) * A * E;
 #pragma unroll
     for (int m = 0; m < RT; ++m)

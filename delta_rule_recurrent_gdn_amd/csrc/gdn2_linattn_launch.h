@@ -16,29 +16,35 @@ static hipError_t launch_lin_s(const LinArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   const int64_t items = (int64_t)a.max_segs * (a.cu ? 1 : a.N) * a.H;
-  const int64_t blocks = (items + 7) / 8 * 8 * ((a.E + Sh::CW - 1) / Sh::CW);
+  const int64_t blocks = (items + 7) / 8 * 8 * ((a.E + Sh::CW - 1) / Sh::CW) * a.sweeps;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(Sh::kThreads), lds, s, a);
   return hipGetLastError();
 }
 
-// The decayed z of the update in three bf16 terms where the state can be an output (fp32 to its last bits; the same
-// whether it is asked for or not, so that r is the same too), in two where it only enters r, whose rounding to bf16
-// is 2^7 times what two terms leave.
+// The decayed z of the update in three bf16 terms where a state can be an output (fp32 to its last bits), in two where
+// it only enters r, whose rounding to bf16 is 2^7 times what two terms leave.
 template <int A, int NW, int NT, bool F32, bool STATE>
 static hipError_t launch_lin_t(const LinArgs& a, hipStream_t s) {
   if constexpr (!F32) {
-    if (!a.sw.exact) return launch_lin_s<A, NW, NT, F32, STATE, 2>(a, s);
+    bool exact = false;
+    for (int i = 0; i < a.sweeps; ++i) exact |= a.sw[i].exact;
+    if (!exact) return launch_lin_s<A, NW, NT, F32, STATE, 2>(a, s);
   }
   return launch_lin_s<A, NW, NT, F32, STATE, 3>(a, s);
 }
+
+// Column tiles a wave at E = 128. The sums of the pieces take both halves of the columns in one workgroup, which reads
+// y once; the sweeps, whose LDS holds one workgroup a CU, take two workgroups.
+template <bool F32, bool STATE>
+constexpr int kLinWide = STATE && !F32 ? 2 : 1;
 
 template <int A, bool F32, bool STATE>
 static hipError_t launch_lin_e(const LinArgs& a, hipStream_t s) {
   switch (a.E) {
     case 16: return launch_lin_t<A, 1, 1, F32, STATE>(a, s);
     case 32: return launch_lin_t<A, 2, 1, F32, STATE>(a, s);
-    case 64:
-    case 128: return launch_lin_t<A, 4, 1, F32, STATE>(a, s);
+    case 64: return launch_lin_t<A, 4, 1, F32, STATE>(a, s);
+    case 128: return launch_lin_t<A, 4, kLinWide<F32, STATE>, F32, STATE>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -95,7 +95,7 @@ def test_workspace_bytes():
     assert size(0, 8, 4096, 16, 16, 128, 128, 0) == 0           # whole sequences fill the GPU
     pieces = size(0, 1, 65536, 16, 16, 128, 128, 0)             # a state a piece and head
     assert pieces > 0 and pieces % (16 * 128 * 128 * 4) == 0
-    assert size(_lib.GDN2_OP_BWD, 8, 4096, 4, 16, 128, 128, 0) == 8 * 4096 * 16 * 128 * 4  # fp32 dq, dk before the shared heads' sum
+    assert size(_lib.GDN2_OP_BWD, 8, 4096, 4, 16, 128, 128, 0) == 2 * 8 * 4096 * 16 * 128 * 4  # fp32 dq, dk of every head
     assert size(0, 3, 1000, 2, 2, 64, 64, 1) > 0
     assert size(0, 0, 64, 2, 2, 64, 64, 0) == size(0, 1, 64, 2, 3, 64, 64, 0) == 0
     assert size(_lib.GDN2_OP_DECODE, 1, 64, 2, 2, 64, 64, 0) == 0
