@@ -332,31 +332,33 @@ struct LinLoader {
   // The n-th score tile of wave w, strip ts against strip jt <= ts, at most three a wave:
   //   w = 0: (3,3) (3,2)   1: (3,1) (3,0) (0,0)   2: (2,2) (2,1) (2,0)   3: (1,1) (1,0)      (chunks of four strips)
   //   w = 0: (1,1)         1: (1,0)               2: (0,0)                                  (two strips)
-  __device__ __forceinline__ static bool tile(int w, int n, int& ts, int& jt) {
-    if constexpr (TT == 4) {
-      ts = w == 0 ? 3 : w == 1 ? (n < 2 ? 3 : 0) : 4 - w;
-      jt = w == 0 ? 3 - n : w == 1 ? (n < 2 ? 1 - n : 0) : 4 - w - n;
-      return n < 2 || w == 1 || w == 2;
-    } else {
-      ts = w < 2 ? 1 : 0;
-      jt = w == 0 ? 1 : 0;
-      return n == 0 && w < 3;
+  static constexpr int strip(int w, int n) {
+    return TT == 4 ? (w == 0 ? 3 : w == 1 ? (n < 2 ? 3 : 0) : 4 - w) : (w < 2 ? 1 : 0);
+  }
+  static constexpr int against(int w, int n) {
+    return TT == 4 ? (w == 0 ? 3 - n : w == 1 ? (n < 2 ? 1 - n : 0) : 4 - w - n) : (w == 0 ? 1 : 0);
+  }
+  static constexpr int tiles(int w) { return TT == 4 ? (w == 1 || w == 2 ? 3 : 2) : (w < 3 ? 1 : 0); }
+  __device__ __forceinline__ void scores(const char* buf, char* tp, int w, int g, int i) {
+    switch (w) {  // one code a wave: its tiles' places are constants
+      case 0: return scores_of<0>(buf, tp, g, i);
+      case 1: return scores_of<1>(buf, tp, g, i);
+      case 2: return scores_of<2>(buf, tp, g, i);
+      default: return scores_of<3>(buf, tp, g, i);
     }
   }
   // scores, transposed: tile (jt, ts) holds tokens j = 16 jt + 4g + r of columns i = 16 ts + l%16
-  __device__ __forceinline__ void scores(const char* buf, char* tp, int w, int g, int i) {
+  template <int W>
+  __device__ __forceinline__ void scores_of(const char* buf, char* tp, int g, int i) {
     const char* const ty = buf;
     const char* const tx = buf + Sh::kBuf;
-    int strip = -1;
     V xv[UK];
 #pragma unroll
-    for (int n = 0; n < (TT == 4 ? 3 : 1); ++n) {
-      int ts, jt;
-      if (!tile(w, n, ts, jt)) break;
-      if (ts != strip) {
+    for (int n = 0; n < tiles(W); ++n) {
+      const int ts = strip(W, n), jt = against(W, n);
+      if (n == 0 || ts != strip(W, n - 1)) {
 #pragma unroll
         for (int u = 0; u < UK; ++u) xv[u] = TX::row(tx, 16 * ts + i, u, g);
-        strip = ts;
       }
       f32x4 p = zero4(), p2 = zero4();  // two sums side by side: half the wait for one another
 #pragma unroll
@@ -579,15 +581,70 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
     }
   };
-  constexpr int MP = RT >= 2 ? 2 : 1, NS = UC * RT / MP;  // tiles a stage of the update, its stages
-  auto y_of = [&](const char* ty, int st, int m) {        // operand of stage st, its tile m
-    const int u = st / (RT / MP), mt = st % (RT / MP) * MP + m;
+  constexpr int MP = RT >= 4 ? 4 : RT, SU = RT / MP, NS = UC * SU;  // tiles a stage of the update, stages a unit, in all
+  auto y_of = [&](const char* ty, int st, int m) {                  // operand of stage st, its tile m
+    const int u = st / SU, mt = st % SU * MP + m;
     return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);
+  };
+  // unit u of the state as an operand, 16 bit: in two terms
+  V zh[2][NT], zl[2][NT];
+  auto state_operand = [&](int u) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (F32) {
+        zh[u & 1][n] = Z[u][n];
+      } else {
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][n][r], x[4 + r] = Z[2 * u + 1][n][r];
+        zh[u & 1][n] = pack_hi(x);
+        sub_hi(x);
+        zl[u & 1][n] = pack_rne(x);
+      }
+    }
+  };
+  // c_j z_j of unit u, 16 bit: in SPLIT terms
+  constexpr int TERMS = F32 ? 1 : SPLIT;
+  V zs[2][TERMS][NT];
+  auto terms = [&](int u) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (F32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zs[u & 1][0][n][e] = cz[u][e] * zv[u][n][e];
+      } else {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
+#pragma unroll
+        for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
+          zs[u & 1][t2][n] = pack_hi(x);
+          sub_hi(x);
+        }
+        zs[u & 1][SPLIT - 1][n] = pack_rne(x);
+      }
+    }
+  };
+  auto decay = [&](int m0) {
+#pragma unroll
+    for (int m = 0; m < MP; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Z[m0 + m][n][r] *= gC;
+  };
+  // The barrier of a step. These waves write nothing to LDS, and what they have read ahead of it stays as it is for
+  // two steps, so they need not wait for it.
+  auto step_barrier = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
   __syncthreads();
   if constexpr (!STATE) __syncthreads();
   int now = 0;  // this chunk's buffer
   fetch(lds);
+  if constexpr (!STATE) state_operand(0);
   for (int s = 0; s < steps; ++s) {
     const char* const ty = lds + now * BUF;
     const char* const tz = ty + Sh::kXY;
@@ -595,49 +652,51 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     const char* const tp = scores + (s & 1) * Sh::kScores;
     const int valid = min(C, t.pos1 - (t.pos0 + s * C));
     const bool last = s + 1 == steps;
+    const bool update = !last || want_last;
     now = now == (STATE ? 1 : 2) ? 0 : now + 1;
     const char* const after = lds + now * BUF;
-    V y[3][MP];
+    if (valid < C && update) {
+      set_cz(valid);
+      chunk_decay(valid, gC, gRest);
+    }
+    auto make_up = [&] {
+      if (valid < C || s % kMakeUp == kMakeUp - 1) {
+        const float rest = valid < C ? gRest : kMakeUp * gRest;
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], rest, Z[m][n][r]);
+      }
+    };
+    V y[2][MP];
+    // r^T from the state and from the scores: rows are columns of the state, columns are tokens
+    f32x4 R[TT][NT], R2[TT][NT];
 
     if constexpr (!STATE) {
       // scores by unit: row tile k, unit u <= 16 k / KU
       constexpr int NU = F32 ? TT * (TT + 1) / 2 : TT * (TT + 2) / 4, H1 = NU / 2;
       V ph[NU], pl[F32 ? 1 : NU];
-      auto get_scores = [&](int from, int to) {
+      auto each_unit = [&](int from, int to, auto f) {
         int n = 0;
 #pragma unroll
         for (int k = 0; k < TT; ++k)
 #pragma unroll
           for (int u = 0; u <= 16 * k / KU; ++u, ++n)
-            if (n >= from && n < to) {
-              ph[n] = TP::row(tp, 16 * k + i, u, g);
-              if constexpr (!F32) pl[n] = TP::row(tp + Sh::kP, 16 * k + i, u, g);
-            }
+            if (n >= from && n < to) f(n, k, u);
+      };
+      auto get_scores = [&](int from, int to) {
+        each_unit(from, to, [&](int n, int k, int u) {
+          ph[n] = TP::row(tp, 16 * k + i, u, g);
+          if constexpr (!F32) pl[n] = TP::row(tp + Sh::kP, 16 * k + i, u, g);
+        });
       };
       const int4 odd4 = *reinterpret_cast<const int4*>(flags + (now == 0 ? 2 : now - 1) * kLinLoad);
-      // r^T from the state and from the scores: rows are columns of the state, columns are tokens
-      f32x4 R[TT][NT], R2[TT][NT];
 #pragma unroll
       for (int k = 0; k < TT; ++k)
 #pragma unroll
         for (int n = 0; n < NT; ++n) R[k][n] = R2[k][n] = zero4();
-      V zh[2][NT], zl[2][NT];
-      auto state_operand = [&](int u) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if constexpr (F32) {
-            zh[u & 1][n] = Z[u][n];
-          } else {
-            float x[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][n][r], x[4 + r] = Z[2 * u + 1][n][r];
-            zh[u & 1][n] = pack_hi(x);
-            sub_hi(x);
-            zl[u & 1][n] = pack_rne(x);
-          }
-        }
-      };
-      state_operand(0);
 #pragma unroll
       for (int u = 0; u < UK; ++u) {
         V xn[TT];
@@ -683,31 +742,31 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
           for (int n = 0; n < NT; ++n) lin_finite(zp[u][n]);
       }
+      make_up();
+      auto add_scores = [&](int from, int to) {
+        if constexpr (!F32)
+          each_unit(from, to, [&](int n, int k, int u) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) lin_mma(R2[k][c], zp[u][c], pl[n]);
+          });
+        each_unit(from, to, [&](int n, int k, int u) {
+#pragma unroll
+          for (int c = 0; c < NT; ++c) lin_mma(R2[k][c], zp[u][c], ph[n]);
+        });
+      };
       get_scores(H1, NU);
       GDN2_LIN_FENCE;
-      auto add_scores = [&](int from, int to) {
-        int n = 0;
-#pragma unroll
-        for (int k = 0; k < TT; ++k)
-#pragma unroll
-          for (int u = 0; u <= 16 * k / KU; ++u, ++n)
-            if (n >= from && n < to) {
-#pragma unroll
-              for (int c = 0; c < NT; ++c) {
-                if constexpr (!F32) lin_mma(R2[k][c], zp[u][c], pl[n]);
-                lin_mma(R2[k][c], zp[u][c], ph[n]);
-              }
-            }
-      };
       add_scores(0, H1);
+      terms(0);
+      GDN2_LIN_MIX((F32 ? 1 : 2) * H1 * NT, 10);
       GDN2_LIN_FENCE;
 #pragma unroll
-      for (int m = 0; m < MP; ++m) {
-        y[0][m] = y_of(ty, 0, m);
-        if (NS > 1) y[1][m] = y_of(ty, 1, m);
-      }
+      for (int m = 0; m < MP; ++m) y[0][m] = y_of(ty, 0, m);
       GDN2_LIN_FENCE;
       add_scores(H1, NU);
+      decay(0);
+      GDN2_LIN_MIX((F32 ? 1 : 2) * (NU - H1) * NT, 3);
+      GDN2_LIN_FENCE;
       if (odd) {
 #pragma unroll
         for (int k = 0; k < TT; ++k)
@@ -731,6 +790,14 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
               }
             }
       }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MP; ++m) y[0][m] = y_of(ty, 0, m);
+      make_up();
+      terms(0);
+      decay(0);
+    }
+    auto store = [&] {
 #pragma unroll
       for (int k = 0; k < TT; ++k) {
         if (valid == C || 16 * k + i < valid) {
@@ -746,66 +813,14 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
         }
       }
       rat += C * rstep;
-    } else {
-#pragma unroll
-      for (int m = 0; m < MP; ++m) {
-        y[0][m] = y_of(ty, 0, m);
-        if (NS > 1) y[1][m] = y_of(ty, 1, m);
-      }
-    }
+    };
 
-    if (!last || want_last) {
-      if (valid < C) {
-        set_cz(valid);
-        chunk_decay(valid, gC, gRest);
-      }
-      if (valid < C || s % kMakeUp == kMakeUp - 1) {
-        const float rest = valid < C ? gRest : kMakeUp * gRest;
-#pragma unroll
-        for (int m = 0; m < RT; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], rest, Z[m][n][r]);
-      }
-      // Z <- g^n Z + sum_j y_j (c_j z_j)^T. 16 bit: c_j z_j in SPLIT terms
-      constexpr int TERMS = F32 ? 1 : SPLIT;
-      V zs[2][TERMS][NT];
-      auto terms = [&](int u) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if constexpr (F32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) zs[u & 1][0][n][e] = cz[u][e] * zv[u][n][e];
-          } else {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
-#pragma unroll
-            for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
-              zs[u & 1][t2][n] = pack_hi(x);
-              sub_hi(x);
-            }
-            zs[u & 1][SPLIT - 1][n] = pack_rne(x);
-          }
-        }
-      };
-      auto decay = [&](int m0) {
-#pragma unroll
-        for (int m = 0; m < MP; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) Z[m0 + m][n][r] *= gC;
-      };
-      constexpr int SU = RT / MP;  // stages a unit
-      terms(0);
-      decay(0);
+    if (update) {  // Z <- g^n Z + sum_j y_j (c_j z_j)^T
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
-        if (st + 2 < NS) {
+        if (st + 1 < NS) {
 #pragma unroll
-          for (int m = 0; m < MP; ++m) y[(st + 2) % 3][m] = y_of(ty, st + 2, m);
+          for (int m = 0; m < MP; ++m) y[(st + 1) & 1][m] = y_of(ty, st + 1, m);
         }
         GDN2_LIN_FENCE;
         const int u = st / SU, m0 = st % SU * MP;
@@ -814,17 +829,22 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
           for (int m = 0; m < MP; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) lin_mma(Z[m0 + m][n], y[st % 3][m], zs[u & 1][t2][n]);
-        // beside the products: the next stage's decay, the next unit's terms
+            for (int n = 0; n < NT; ++n) lin_mma(Z[m0 + m][n], y[st & 1][m], zs[u & 1][t2][n]);
+        // beside the products: the next stage's decay, the next unit's terms, the next chunk's first operand
         if (st + 1 < SU) decay(m0 + MP);
         if (st % SU == SU - 1 && u + 1 < UC) terms(u + 1);
+        if (!STATE && SU > 1 && st == NS - 1) state_operand(0);
         GDN2_LIN_MIX(TERMS * MP * NT, 4);
         GDN2_LIN_FENCE;
+        if (!STATE && st == 0) store();
       }
+      if (!STATE && SU == 1) state_operand(0);
+    } else if (!STATE) {
+      store();
     }
     if constexpr (!STATE) {  // the next chunk is in LDS since the step before
       if (!last) fetch(after);
-      __syncthreads();
+      step_barrier();
     } else {
       __syncthreads();
       if (!last) fetch(after);

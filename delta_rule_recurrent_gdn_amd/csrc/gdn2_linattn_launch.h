@@ -33,18 +33,13 @@ static hipError_t launch_lin_t(const LinArgs& a, hipStream_t s) {
   return launch_lin_s<A, NW, NT, F32, STATE, 3>(a, s);
 }
 
-// Column tiles a wave at E = 128. The sums of the pieces take both halves of the columns in one workgroup, which reads
-// y once; the sweeps, whose LDS holds one workgroup a CU, take two workgroups.
-template <bool F32, bool STATE>
-constexpr int kLinWide = STATE && !F32 ? 2 : 1;
-
 template <int A, bool F32, bool STATE>
 static hipError_t launch_lin_e(const LinArgs& a, hipStream_t s) {
   switch (a.E) {
     case 16: return launch_lin_t<A, 1, 1, F32, STATE>(a, s);
     case 32: return launch_lin_t<A, 2, 1, F32, STATE>(a, s);
-    case 64: return launch_lin_t<A, 4, 1, F32, STATE>(a, s);
-    case 128: return launch_lin_t<A, 4, kLinWide<F32, STATE>, F32, STATE>(a, s);
+    case 64:
+    case 128: return launch_lin_t<A, 4, 1, F32, STATE>(a, s);
   }
   return hipErrorInvalidValue;
 }
