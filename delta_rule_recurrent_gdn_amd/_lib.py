@@ -80,6 +80,7 @@ SIGNATURES = {
     "gdn2_linattn_fwd_varlen": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I, _F, _I, _P]),
     "gdn2_linattn_bwd_varlen": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I,
                                      _F, _I, _P]),
+    "gdn2_varlen_zero_outside": (_I, [_P, _P, _I, _I, _SZ, _P]),
     "gdn2_linattn_decode_step": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
     "gdn2_linattn_decode_step_slots": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
     "gdn2_qk_norm_rope_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _L, _L, _I, _I, _I, _I, _L, _L, _L, _L, _F, _F, _I,

@@ -51,6 +51,11 @@ struct LinArgs {
 
 int linattn_seg_tokens(int N, int T, int H, int E, int sweeps, bool packed, bool f32);
 int linattn_max_segs(int N, int T, int seg_tok, bool packed);
+// a packed batch's tables, built on the device from the caller's offsets; sets a's pointers to them
+size_t linattn_table_bytes(int N, int max_segs);
+hipError_t launch_linattn_plan(const int64_t* cu, char* tables, LinArgs& a, hipStream_t s);
+// zeros in the rows [row_bytes] of x outside every sequence
+hipError_t launch_linattn_outside(void* x, const int64_t* cu, int N, int64_t T, int64_t row_bytes, hipStream_t s);
 // piece states of the sweeps, joined and handed to the sweeps' pieces, then the sweeps themselves
 hipError_t launch_linattn_sweeps(const LinArgs& a, hipStream_t s);
 // dst[row, j, :] = sum over i < G of src[row, j G + i, :] (src fp32), rounded to the type of dst; packed

@@ -53,7 +53,7 @@ Plan plan(bool bwd, int N, int T, int Hk, int H, int Dk, int Dv, bool packed, in
   p.seg_tok = gdn2::linattn_seg_tokens(N, T, H, E, bwd ? 2 : 1, packed, dt == GDN2_F32);
   p.max_segs = gdn2::linattn_max_segs(N, T, p.seg_tok, packed);
   p.pieces = packed ? p.seg_tok < T : p.max_segs > 1;
-  p.states = packed ? al256(gdn2::varlen_table_bytes(N, T, p.seg_tok, 0)) : 0;
+  p.states = packed ? gdn2::linattn_table_bytes(N, p.max_segs) : 0;
   const size_t slots = (size_t)p.max_segs * (packed ? 1 : N);
   p.state_bytes = p.pieces ? al256(slots * H * Dk * Dv * 4) : 0;
   p.partial = p.states + sweeps * p.state_bytes;
@@ -94,15 +94,7 @@ int begin(const Call& c, bool bwd, Plan& p, gdn2::LinArgs& a) {
   a.pieces = p.pieces;
   a.seg_tok = p.seg_tok;
   a.max_segs = p.max_segs;
-  if (c.cu) {
-    gdn2::Varlen vl;
-    const hipError_t e = gdn2::launch_varlen_plan(reinterpret_cast<const int64_t*>(c.cu), c.N, c.T, p.seg_tok, 0, c.ws,
-                                                  vl, c.stream);
-    if (e != hipSuccess) return GDN2_ERR_HIP;
-    a.cu = vl.cu;
-    a.seg_first = vl.chunk_first;
-    a.seg_seq = vl.chunk_seq;
-  }
+  if (c.cu) return hip_status(gdn2::launch_linattn_plan(reinterpret_cast<const int64_t*>(c.cu), c.ws, a, c.stream));
   return GDN2_OK;
 }
 
@@ -173,6 +165,7 @@ int backward(const Call& c, const void* dO, const float* dS_final, void* dq, voi
   a.sw[1] = sk;
   a.sw[2] = sv;
   a.sweeps = c.Dk == c.Dv && !apart ? 3 : 2;
+  a.sw[0].exact = apart && c.Dk == c.Dv;  // as in one launch with dS0's: the same bits either way
   e = gdn2::launch_linattn_sweeps(a, c.stream);
   if (e == hipSuccess && a.sweeps == 2) {
     a.A = c.Dk;
@@ -281,6 +274,15 @@ int gdn2_linattn_bwd_varlen(const void* q, const void* k, const void* v, const f
   if (!aligned(cu_seqlens, 8)) return GDN2_ERR_ALIGN;
   return backward(call(q, k, v, log_decay, cu_seqlens, S0, N, T, Hk, H, Dk, Dv, scale, dt, workspace, workspace_bytes,
                        stream), dO, dS_final, dq, dk, dv, dS0);
+}
+
+int gdn2_varlen_zero_outside(void* x, const long long* cu_seqlens, int N, int T, size_t row_bytes, void* stream) {
+  if (N < 0 || T < 0) return GDN2_ERR_SHAPE;
+  if (N == 0 || T == 0 || row_bytes == 0) return GDN2_OK;
+  if (x == nullptr || cu_seqlens == nullptr) return GDN2_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(cu_seqlens, 8) || row_bytes % 16 != 0) return GDN2_ERR_ALIGN;
+  return hip_status(gdn2::launch_linattn_outside(x, reinterpret_cast<const int64_t*>(cu_seqlens), N, T,
+                                                 (int64_t)row_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int gdn2_linattn_decode_step(const void* q, const void* k, const void* v, const float* log_decay, float* S, void* o,

@@ -107,13 +107,25 @@ def _packed(q, cu_seqlens):
     return cu_seqlens.numel() - 1
 
 
+def _new(shape, dtype, device, cu, N):
+    """An output: of a packed batch, with zeros in the rows outside every sequence, which the kernels do not write."""
+    if cu is None or N == 0:
+        return (torch.empty if cu is None else torch.zeros)(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    row = shape[2] * shape[3] * t.element_size()
+    with _on(device):
+        st = _lib.load().gdn2_varlen_zero_outside(t.data_ptr(), cu.data_ptr(), N, shape[1], row, _stream(device))
+    _lib.check(st, "gdn2_varlen_zero_outside")
+    return t
+
+
 def _forward(q, k, v, log_decay, cu, S0, scale, want_final_state, o, workspace):
     lib = _lib.load()
     dt, dev, (B, T), Hk, H, Dk, Dv = _sizes(q, k, v, log_decay, 4)
     N = B if cu is None else _packed(q, cu)
     _state("S0", S0, (N, H, Dk, Dv), dev)
-    if o is None:  # rows outside every packed sequence are not written
-        o = (torch.empty if cu is None else torch.zeros)((B, T, H, Dv), dtype=q.dtype, device=dev)
+    if o is None:
+        o = _new((B, T, H, Dv), q.dtype, dev, cu, N)
     else:
         _like("o", o, (B, T, H, Dv), q.dtype, dev)
     S_final = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev) if want_final_state else None
@@ -152,8 +164,7 @@ def _backward(q, k, v, log_decay, dO, cu, S0, dS_final, scale, want_dS0, workspa
     _like("dO", dO, v.shape, q.dtype, dev)
     _state("S0", S0, (N, H, Dk, Dv), dev)
     _state("dS_final", dS_final, (N, H, Dk, Dv), dev)
-    new = torch.empty if cu is None else torch.zeros  # rows outside every packed sequence are not written
-    g = {n: new(t.shape, dtype=q.dtype, device=dev) for n, t in (("dq", q), ("dk", q), ("dv", v))}
+    g = {n: _new(t.shape, q.dtype, dev, cu, N) for n, t in (("dq", q), ("dk", q), ("dv", v))}
     g["dS0"] = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=dev) if want_dS0 else None
     need = lib.gdn2_linattn_workspace_bytes(_lib.GDN2_OP_BWD, N, T, Hk, H, Dk, Dv, int(cu is not None), dt)
     ws, ws_bytes, keep = _scratch(workspace, need, dev)

@@ -30,14 +30,17 @@ def _rows(name, t, like=None):
     if (D > 1 and stride[-1] != 1) or (heads > 1 and stride[-2] != D):
         raise ValueError(f"{name}'s heads must lie side by side (strides {stride})")
     rows, step, want = 1, None, None
-    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+    for d in range(len(shape) - 3, -1, -1):
+        n = shape[d]
         if n != 1:
             if step is None:
-                step = s
-            elif s != want:
+                step = stride[d]
+                want = step * n
+            elif stride[d] != want:
                 raise ValueError(f"{name}'s rows must be evenly spaced (strides {stride})")
-            want = s * n
-        rows *= n
+            else:
+                want *= n
+            rows *= n
     return rows, heads, D, heads * D if step is None else step
 
 

@@ -421,6 +421,9 @@ int gdn2_linattn_bwd_varlen(const void* q, const void* k, const void* v, const f
                             const float* dS_final, void* dq, void* dk, void* dv, float* dS0, void* workspace,
                             size_t workspace_bytes, int T, int Hk, int H, int Dk, int Dv, float scale, int dt,
                             void* stream);
+/* Zeros in the rows of a packed tensor [T, row_bytes] outside every sequence (the rows that the packed calls leave
+ * unwritten), for callers that hand over fresh memory. N = 0 does nothing. row_bytes a multiple of 16. */
+int gdn2_varlen_zero_outside(void* x, const long long* cu_seqlens, int N, int T, size_t row_bytes, void* stream);
 int gdn2_linattn_decode_step(const void* q, const void* k, const void* v, const float* log_decay, float* S, void* o,
                              int B, int Hk, int H, int Dk, int Dv, float scale, int dt, void* stream);
 int gdn2_linattn_decode_step_slots(const void* q, const void* k, const void* v, const float* log_decay, float* S_pool,

@@ -211,6 +211,57 @@ def test_packed_offsets_out_of_order_stay_inside():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_many_packed_sequences():
+    """150 sequences (more than the planner takes at a time), empty ones among them, against each sequence alone."""
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    g = torch.Generator().manual_seed(31)
+    lens = torch.randint(0, 40, (150,), generator=g)
+    lens[::7] = 0
+    lens[64], lens[128] = 400, 300
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    T = int(cu[-1]) + 3
+    x = dev(make(32, 1, T, 1, 2, 32, 32, F32))
+    S0 = torch.randn(150, 2, 32, 32, device="cuda")
+    o, S = gdn.gdn2_linattn_fwd_varlen(x["q"], x["k"], x["v"], x["ld"], cu.cuda(), S0=S0)
+    r = gdn.gdn2_linattn_bwd_varlen(x["q"], x["k"], x["v"], x["ld"], x["dO"], cu.cuda(), S0=S0)
+    for n in range(150):
+        a, b = int(cu[n]), int(cu[n + 1])
+        part = [x[m][:, a:b].contiguous() for m in ("q", "k", "v")]
+        o1, S1 = gdn.gdn2_linattn_fwd_chunked(*part, x["ld"], S0=S0[n:n + 1])
+        r1 = gdn.gdn2_linattn_bwd_chunked(*part, x["ld"], x["dO"][:, a:b].contiguous(), S0=S0[n:n + 1])
+        near = lambda s, t: torch.testing.assert_close(s, t, rtol=0, atol=1e-5 * (1 + float(t.abs().max()) if t.numel() else 1))  # noqa: E731
+        near(o[:, a:b], o1)
+        near(S[n:n + 1], S1)
+        near(r["dS0"][n:n + 1], r1["dS0"])
+        for m in ("dq", "dk", "dv"):
+            near(r[m][:, a:b], r1[m])
+    assert (o[:, T - 3:] == 0).all() and all((r[m][:, T - 3:] == 0).all() for m in ("dq", "dk", "dv"))
+
+
+def test_gradient_of_the_first_state_in_place():
+    """dS0 in the memory of S0 or of dS_final."""
+    from delta_rule_recurrent_gdn_amd import _lib
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    for T in (100, 1500):
+        x = dev(make(33, 1, T, 1, 1, 32, 32, BF16))
+        want = gdn.gdn2_linattn_bwd_chunked(x["q"], x["k"], x["v"], x["ld"], x["dO"], S0=x["S0"], dS_final=x["dS"])
+        p = lambda t: t.data_ptr()  # noqa: E731
+        need = gdn.gdn2_linattn_workspace_bytes(_lib.GDN2_OP_BWD, 1, T, 1, 1, 32, 32, BF16)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        for name in ("S0", "dS"):
+            s = {n: x[n].clone() for n in ("S0", "dS")}
+            d = [torch.empty_like(x[n]) for n in ("q", "k", "v")]
+            st = _lib.load().gdn2_linattn_bwd_chunked(
+                p(x["q"]), p(x["k"]), p(x["v"]), p(x["ld"]), p(s["S0"]), p(x["dO"]), p(s["dS"]), p(d[0]), p(d[1]), p(d[2]),
+                p(s[name]), p(ws), ws.numel(), 1, T, 1, 1, 32, 32, 1.0, _lib.GDN2_BF16,
+                torch.cuda.current_stream().cuda_stream)
+            assert st == 0 and torch.equal(s[name], want["dS0"])
+            for got, n in zip(d, ("dq", "dk", "dv")):
+                assert torch.equal(got, want[n])
+
+
 def test_empty_calls():
     import delta_rule_recurrent_gdn_amd as gdn
 

@@ -89,6 +89,15 @@ def test_refusals(call, kw, status):
     assert call(**kw) == status
 
 
+@pytest.mark.parametrize("args,status", [
+    ((None, A, 2, 8, 64), NULL), ((A, None, 2, 8, 64), NULL), ((A + 8, A, 2, 8, 64), ALIGN), ((A, A + 4, 2, 8, 64), ALIGN),
+    ((A, A, 2, 8, 40), ALIGN), ((A, A, -1, 8, 64), SHAPE), ((A, A, 2, -8, 64), SHAPE), ((None, None, 0, 8, 64), OK),
+    ((None, None, 2, 0, 64), OK),
+])
+def test_zero_outside_refusals(args, status):
+    assert _lib.load().gdn2_varlen_zero_outside(*args, None) == status
+
+
 def test_workspace_bytes():
     lib = _lib.load()
     size = lambda op, N, T, Hk, H, Dk, Dv, packed: lib.gdn2_linattn_workspace_bytes(op, N, T, Hk, H, Dk, Dv, packed, 1)  # noqa: E731
