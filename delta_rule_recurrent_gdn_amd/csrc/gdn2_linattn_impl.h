@@ -66,8 +66,9 @@ __device__ __forceinline__ void lin_mma(f32x4& acc, const f32x4& a, const f32x4&
 // served 16 lanes at a time, 8-byte ones 32, 4-byte ones 64). How a tile is read decides which bits of the row go
 // where; rows narrower than 16 blocks share the banks' width, which separates their lowest bits already:
 //   kRows: 16 bytes of 16 neighbouring rows (x, the scores);
-//   kBoth: 16 bit: 8 bytes of rows 0-3 and 8-11 of 16, in 4 neighbouring blocks each (the transposing read), and
-//          8 bytes of 16 neighbouring rows, in 2 blocks; one bit exchanges the halves of a block (y);
+//   kBoth: that, and, 16 bit, 8 bytes of rows 0-3 and 8-11 of 16, in 4 neighbouring blocks each (the transposing read
+//          of y). The latter meets itself once in its banks; exchanging the halves of a block in some rows avoids
+//          that, but costs more vector instructions than it saves (forward 160 us either way);
 //   kCols: 16 bit: 32 bytes of rows 0-3 and 8-11 (z).
 // fp32 reads down the rows 4 bytes wide: 16 columns of rows 4 apart.
 enum LinUse { kRows, kBoth, kCols };
@@ -78,35 +79,22 @@ struct LinTile {
   using V = typename Op::V;
   static constexpr int kRow = W * Op::ES;       // bytes a row
   static constexpr int NB = kRow / 16;          // blocks a row
-  static constexpr bool kSwap = !F32 && USE == kBoth;
   __device__ __forceinline__ static int bit(int r, int from, int to) { return ((r >> from) & 1) << to; }
   __device__ __forceinline__ static int perm(int r) {
     if constexpr (F32) return NB >= 16 ? (r & 15) : NB == 8 ? bit(r, 2, 2) | bit(r, 3, 1) | bit(r, 1, 0) : (r >> 2) & 3;
     else if constexpr (USE == kRows) return NB >= 16 ? (r & 15) : NB == 8 ? (r >> 1) & 7 : (r >> 2) & 3;
     else if constexpr (USE == kBoth)
-      return NB >= 16 ? bit(r, 3, 3) | bit(r, 0, 2) | bit(r, 2, 1) : NB == 8 ? bit(r, 3, 2) | bit(r, 2, 1) : bit(r, 2, 1);
+      return NB >= 16 ? bit(r, 3, 3) | bit(r, 0, 2) | bit(r, 1, 1) | bit(r, 2, 0)
+             : NB == 8 ? bit(r, 3, 2) | bit(r, 1, 1) | bit(r, 2, 0) : bit(r, 3, 1) | bit(r, 2, 0);
     else
       return NB >= 16 ? bit(r, 3, 3) | bit(r, 1, 2) | bit(r, 0, 1) : NB == 8 ? bit(r, 3, 2) | bit(r, 1, 1)
              : NB == 4 ? bit(r, 3, 1) : 0;
   }
-  __device__ __forceinline__ static bool swapped(int r) { return kSwap && ((r >> (NB >= 8 ? 1 : 3)) & 1); }
-  // byte offset of block b of row r, of its 8-byte half h
+  // byte offset of block b of row r
   __device__ __forceinline__ static int at(int r, int b) { return r * kRow + ((b ^ perm(r)) << 4); }
-  __device__ __forceinline__ static int at(int r, int b, int h) { return at(r, b) + ((h ^ (int)swapped(r)) << 3); }
-  __device__ __forceinline__ static void put(char* t, int r, int b, uint4 v) {
-    const bool x = swapped(r);
-    *reinterpret_cast<uint4*>(t + at(r, b)) =
-        make_uint4(x ? v.z : v.x, x ? v.w : v.y, x ? v.x : v.z, x ? v.y : v.w);
-  }
   // operand of unit u from row r (contraction along the row), lane group g
   __device__ __forceinline__ static V row(const char* t, int r, int u, int g) {
-    if constexpr (kSwap) {
-      const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + at(r, 4 * u + g, 0));
-      const bf16x4 hi = *reinterpret_cast<const bf16x4*>(t + at(r, 4 * u + g, 1));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-      return *reinterpret_cast<const V*>(t + at(r, 4 * u + g));
-    }
+    return *reinterpret_cast<const V*>(t + at(r, 4 * u + g));
   }
   // Operand whose contraction runs down the rows, 16 bit: 32u + 8g .. + 7, fp32: 16u + 4g .. + 3, of 16 columns.
   // 16 bit: the read takes, for every 16 lanes, 4 rows x 16 columns, lane 4 e + p giving the address of row e,
@@ -121,10 +109,10 @@ struct LinTile {
       return v;
     } else {
       const int r = 32 * u + 8 * g + (i >> 2), p = i & 3;
-      const int b = USE == kBoth ? b0 + p : b0 + (p >> 1), half = USE == kBoth ? h : p & 1;
+      const int b = USE == kBoth ? b0 + p : b0 + (p >> 1), half = 8 * (USE == kBoth ? h : p & 1);
       typedef __attribute__((address_space(3))) bf16x4 lds4;
-      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r, b, half)));
-      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r + 4, b, half)));
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r, b) + half));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(t + at(r + 4, b) + half));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
@@ -174,7 +162,7 @@ struct LinFetch {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
       if (TOTAL % NTH == 0 || row + p * RP < Op::C)
-        Tile::put(tile, row + p * RP, tid % NB, v[p]);
+        *reinterpret_cast<uint4*>(tile + Tile::at(row + p * RP, tid % NB)) = v[p];
   }
   // any element of the valid rows is an infinity or NaN (after store)
   __device__ __forceinline__ bool non_finite(const Data& v) const {
@@ -309,7 +297,7 @@ struct LinLoader {
   LinFetch<F32, Sh::CW, Sh::CW, kCols, 64 * kLinLoad> fz;
   float pd[4], pm[4], g16;
 
-  // a chunk's rows in registers; two of these are on their way at a time
+  // a chunk's rows in registers
   struct Rows {
     typename decltype(fx)::Data x, y;
     typename decltype(fz)::Data z;
@@ -398,8 +386,9 @@ struct LinLoader {
 // piece for the join kernel. Otherwise the sweep of one piece.
 //
 // The first NW waves hold the state, the other kLinLoad work ahead of them: in the step in which the state's waves take
-// chunk s, they form the scores of chunk s + 1 (which do not depend on the state), write chunk s + 2 to LDS and send
-// for chunk s + 4, with one barrier a step. (STATE: no scores, chunk s + 1 to LDS, s + 3 sent for.)
+// chunk s, they write chunk s + 2 to LDS, send for chunk s + 3 and form the scores of chunk s + 1 (which do not depend
+// on the state), with one barrier a step; in this order the rows are on their way while the scores are formed (161 us
+// against 167 for a B8 H16 T4096 d128 forward). (STATE: no scores, chunk s + 1 to LDS, s + 2 sent for.)
 template <int A, int NW, int NT, bool F32, bool STATE, int SPLIT>
 __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
   using Sh = LinShape<A, NW, NT, F32>;
@@ -453,9 +442,8 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     ld.fz.begin(static_cast<const char*>(sw.z) + ((int64_t)(t.h / sw.zdiv) * E + cg * CW) * ES, rbz, t.tok0, dir,
                 t.pos0, tid);
     auto valid = [&](int s) { return min(C, t.pos1 - (t.pos0 + s * C)); };
-    typename decltype(ld)::Rows r0, r1;
-    ld.load(r0, valid(0));
-    if (steps > 1) ld.load(r1, valid(1));
+    typename decltype(ld)::Rows rows;
+    ld.load(rows, valid(0));
     if constexpr (!STATE) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {  // token i of its tile against token 4g + r of the same tile, of the one before
@@ -465,37 +453,29 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       }
       ld.g16 = decay_pow(l2, 16);
     }
-    ld.store(r0, lds, flags, lw, valid(0));
-    if (steps > 2) ld.load(r0, valid(2));
+    ld.store(rows, lds, flags, lw, valid(0));
+    if (steps > 1) ld.load(rows, valid(1));
     if constexpr (STATE) {
       __syncthreads();
-      auto step = [&](int s, typename decltype(ld)::Rows& r) {
-        if (s + 1 < steps) ld.store(r, lds + ((s + 1) & 1) * BUF, flags, lw, valid(s + 1));
-        if (s + 3 < steps) ld.load(r, valid(s + 3));
+      for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) ld.store(rows, lds + ((s + 1) & 1) * BUF, flags, lw, valid(s + 1));
+        if (s + 2 < steps) ld.load(rows, valid(s + 2));
         __syncthreads();
-      };
-      for (int s = 0; s < steps; s += 2) {
-        step(s, r1);
-        if (s + 1 < steps) step(s + 1, r0);
       }
     } else {
-      if (steps > 1) ld.store(r1, lds + BUF, flags + kLinLoad, lw, valid(1));
-      if (steps > 3) ld.load(r1, valid(3));
+      if (steps > 1) ld.store(rows, lds + BUF, flags + kLinLoad, lw, valid(1));
+      if (steps > 2) ld.load(rows, valid(2));
       __syncthreads();
       ld.scores(lds, scores, lw, g, i);
       __syncthreads();
       int next = 1, after = 2;  // buffers of chunks s + 1, s + 2
-      auto step = [&](int s, typename decltype(ld)::Rows& r) {
+      for (int s = 0; s < steps; ++s) {
+        if (s + 2 < steps) ld.store(rows, lds + after * BUF, flags + after * kLinLoad, lw, valid(s + 2));
+        if (s + 3 < steps) ld.load(rows, valid(s + 3));
         if (s + 1 < steps) ld.scores(lds + next * BUF, scores + ((s + 1) & 1) * Sh::kScores, lw, g, i);
-        if (s + 2 < steps) ld.store(r, lds + after * BUF, flags + after * kLinLoad, lw, valid(s + 2));
-        if (s + 4 < steps) ld.load(r, valid(s + 4));
         next = after;
         after = after == 2 ? 0 : after + 1;
         __syncthreads();
-      };
-      for (int s = 0; s < steps; s += 2) {
-        step(s, r0);
-        if (s + 1 < steps) step(s + 1, r1);
       }
     }
     return;
@@ -560,14 +540,6 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   int64_t rat = t.tok0 * a.H * E + (t.pos0 + i) * rstep + (int64_t)t.h * E + e0 + 4 * g;
 
   const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
-  // Operands are read from LDS a stage ahead of their products, which the fences keep apart.
-#define GDN2_LIN_FENCE __builtin_amdgcn_sched_barrier(0)
-  // in turn one matrix product and V vector instructions, N times: they run side by side
-#define GDN2_LIN_MIX(N, V)                                 \
-  _Pragma("unroll") for (int mix = 0; mix < (N); ++mix) {  \
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);       \
-    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);       \
-  }
   V zv[UC][NT];  // this wave's columns of z, contraction over tokens
   V xv[TT];      // rows of x, unit 0
   auto fetch = [&](const char* buf) {
@@ -652,10 +624,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     const char* const tp = scores + (s & 1) * Sh::kScores;
     const int valid = min(C, t.pos1 - (t.pos0 + s * C));
     const bool last = s + 1 == steps;
-    const bool update = !last || want_last;
     now = now == (STATE ? 1 : 2) ? 0 : now + 1;
     const char* const after = lds + now * BUF;
-    if (valid < C && update) {
+    if (valid < C) {
       set_cz(valid);
       chunk_decay(valid, gC, gRest);
     }
@@ -706,7 +677,6 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
         } else {
           get_scores(0, H1);
         }
-        GDN2_LIN_FENCE;
 #pragma unroll
         for (int k = 0; k < TT; ++k)
 #pragma unroll
@@ -717,11 +687,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
             for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zl[u & 1][n], xv[k]);
         }
-        if (u + 1 < UK) {
-          state_operand(u + 1);  // beside the products
-          GDN2_LIN_MIX((F32 ? 1 : 2) * TT * NT, 4);
-        }
-        GDN2_LIN_FENCE;
+        if (u + 1 < UK) state_operand(u + 1);  // beside the products
         if (u + 1 < UK) {
 #pragma unroll
           for (int k = 0; k < TT; ++k) xv[k] = xn[k];
@@ -755,18 +721,12 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
         });
       };
       get_scores(H1, NU);
-      GDN2_LIN_FENCE;
       add_scores(0, H1);
       terms(0);
-      GDN2_LIN_MIX((F32 ? 1 : 2) * H1 * NT, 10);
-      GDN2_LIN_FENCE;
 #pragma unroll
       for (int m = 0; m < MP; ++m) y[0][m] = y_of(ty, 0, m);
-      GDN2_LIN_FENCE;
       add_scores(H1, NU);
       decay(0);
-      GDN2_LIN_MIX((F32 ? 1 : 2) * (NU - H1) * NT, 3);
-      GDN2_LIN_FENCE;
       if (odd) {
 #pragma unroll
         for (int k = 0; k < TT; ++k)
@@ -815,14 +775,15 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       rat += C * rstep;
     };
 
-    if (update) {  // Z <- g^n Z + sum_j y_j (c_j z_j)^T
+    // Z <- g^n Z + sum_j y_j (c_j z_j)^T, for the last chunk too where nothing asks for it: a branch here would have the
+    // compiler move the terms above, which run beside the products of r, down into it
+    {
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
         if (st + 1 < NS) {
 #pragma unroll
           for (int m = 0; m < MP; ++m) y[(st + 1) & 1][m] = y_of(ty, st + 1, m);
         }
-        GDN2_LIN_FENCE;
         const int u = st / SU, m0 = st % SU * MP;
 #pragma unroll
         for (int t2 = TERMS - 1; t2 >= 0; --t2)
@@ -834,13 +795,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
         if (st + 1 < SU) decay(m0 + MP);
         if (st % SU == SU - 1 && u + 1 < UC) terms(u + 1);
         if (!STATE && SU > 1 && st == NS - 1) state_operand(0);
-        GDN2_LIN_MIX(TERMS * MP * NT, 4);
-        GDN2_LIN_FENCE;
         if (!STATE && st == 0) store();
       }
       if (!STATE && SU == 1) state_operand(0);
-    } else if (!STATE) {
-      store();
     }
     if constexpr (!STATE) {  // the next chunk is in LDS since the step before
       if (!last) fetch(after);
@@ -850,8 +807,6 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       if (!last) fetch(after);
     }
   }
-#undef GDN2_LIN_FENCE
-#undef GDN2_LIN_MIX
 
   if (want_last) {
     float* dst = STATE ? sw.seg_state + ((int64_t)(a.cu ? t.slot + 1 : t.slot + a.N) * a.H + t.h) * A * E
