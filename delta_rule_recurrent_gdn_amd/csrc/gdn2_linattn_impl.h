@@ -9,10 +9,9 @@
 // gradient of the state (so the gradient of the last state enters as it is). Every power of g has an exponent
 // >= 0, so nothing overflows for g <= 1 whatever the decay, and no quotient of decays is formed.
 //
-// Work: one workgroup per (sequence, head, piece, column group of E); each wave owns 16 NT columns of the state in
-// fp32 accumulators and walks its piece chunk by chunk. Per chunk: x, y, z go to LDS (the next chunk's are in
-// flight in registers meanwhile), the waves share the C x C scores (one 16-token strip each), and every wave forms
-// its columns of r = scores z + decayed x Z and of the state update.
+// Work: one workgroup per (sequence, head, piece, column group of E), which walks its piece chunk by chunk. Per chunk
+// x, y, z go to LDS and the C x C scores are formed once; each wave of the state owns 16 of its columns in fp32
+// accumulators and forms its columns of r = scores z + decayed x Z and of the state update.
 //
 // Operands. A 16x16 accumulator tile holds rows 4g+r of column l%16 (g = l/16), and either operand of a product
 // takes 8 contraction indices (16 bit; fp32: 4) of row or column l%16 from a lane. State tiles 2u, 2u+1 hold the
@@ -215,11 +214,11 @@ __device__ __forceinline__ void lin_finite(f32x4& x) {
 
 constexpr int kLinLoad = 4;  // waves that load and form the scores
 
-template <int A, int NW, int NT, bool F32>
+template <int A, int NW, bool F32>
 struct LinShape {
   using Op = LinOp<F32>;
   static constexpr int AP = A < Op::KU ? Op::KU : A;  // channels of x, y in LDS (16-bit: at least one unit)
-  static constexpr int CW = 16 * NT * NW;             // columns a workgroup
+  static constexpr int CW = 16 * NW;                  // columns a workgroup
   static constexpr int kXY = Op::C * AP * Op::ES;
   static constexpr int kZ = Op::C * CW * Op::ES;
   static constexpr int kP = Op::C * Op::C * Op::ES;
@@ -283,9 +282,9 @@ __device__ __forceinline__ int lin_state_row(int m, int g, int r) {
 }
 
 // The loading waves: the rows of a chunk from memory to LDS, and the scores of a chunk in LDS.
-template <int A, int NW, int NT, bool F32, bool STATE>
+template <int A, int NW, bool F32, bool STATE>
 struct LinLoader {
-  using Sh = LinShape<A, NW, NT, F32>;
+  using Sh = LinShape<A, NW, F32>;
   using Op = LinOp<F32>;
   using V = typename Op::V;
   static constexpr int C = Op::C, UK = Sh::AP / Op::KU, TT = C / 16;
@@ -389,9 +388,9 @@ struct LinLoader {
 // chunk s, they write chunk s + 2 to LDS, send for chunk s + 3 and form the scores of chunk s + 1 (which do not depend
 // on the state), with one barrier a step; in this order the rows are on their way while the scores are formed (161 us
 // against 167 for a B8 H16 T4096 d128 forward). (STATE: no scores, chunk s + 1 to LDS, s + 2 sent for.)
-template <int A, int NW, int NT, bool F32, bool STATE, int SPLIT>
-__global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
-  using Sh = LinShape<A, NW, NT, F32>;
+template <int A, int NW, bool F32, bool STATE, int SPLIT>
+__global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
+  using Sh = LinShape<A, NW, F32>;
   using Op = LinOp<F32>;
   using V = typename Op::V;
   constexpr int C = Op::C, KU = Op::KU, ES = Op::ES, AP = Sh::AP, CW = Sh::CW;
@@ -435,7 +434,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     const int lw = w - NW, tid = threadIdx.x - 64 * NW;
     const int64_t rbx = (int64_t)(a.H / sw.xdiv) * A * ES, rby = (int64_t)(a.H / sw.ydiv) * A * ES;
     const int64_t rbz = (int64_t)(a.H / sw.zdiv) * E * ES;
-    LinLoader<A, NW, NT, F32, STATE> ld;
+    LinLoader<A, NW, F32, STATE> ld;
     if constexpr (!STATE)
       ld.fx.begin(static_cast<const char*>(sw.x) + (int64_t)(t.h / sw.xdiv) * A * ES, rbx, t.tok0, dir, t.pos0, tid);
     ld.fy.begin(static_cast<const char*>(sw.y) + (int64_t)(t.h / sw.ydiv) * A * ES, rby, t.tok0, dir, t.pos0, tid);
@@ -481,8 +480,8 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     return;
   }
 
-  const int c0 = w * 16 * NT, e0 = cg * CW + c0;  // this wave's first column in the tile, in the state
-  float cz[UC][EZ];  // powers of the decay in the update, token KU u + EZ g + e
+  const int c0 = 16 * w, e0 = cg * CW + c0;  // this wave's first column in the tile, in the state
+  float cz[UC][EZ];                          // powers of the decay in the update, token KU u + EZ g + e
   auto set_cz = [&](int n) {
 #pragma unroll
     for (int u = 0; u < UC; ++u)
@@ -507,11 +506,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   }
 
   // the entering state
-  f32x4 Z[RT][NT];
+  f32x4 Z[RT];
 #pragma unroll
-  for (int m = 0; m < RT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) Z[m][n] = zero4();
+  for (int m = 0; m < RT; ++m) Z[m] = zero4();
   if constexpr (!STATE) {
     const float* src = nullptr;
     int rs = E, cs = 1;
@@ -526,12 +523,10 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
       for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = lin_state_row<F32>(m, g, r);
-            if (A >= KU || row < A) Z[m][n][r] = src[(int64_t)row * rs + (int64_t)(e0 + 16 * n + i) * cs];
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int row = lin_state_row<F32>(m, g, r);
+          if (A >= KU || row < A) Z[m][r] = src[(int64_t)row * rs + (int64_t)(e0 + i) * cs];
+        }
     }
   }
 
@@ -539,15 +534,12 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
   const int64_t rstep = dir * (int64_t)a.H * E;  // elements from row to row of the walk
   int64_t rat = t.tok0 * a.H * E + (t.pos0 + i) * rstep + (int64_t)t.h * E + e0 + 4 * g;
 
-  const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
-  V zv[UC][NT];  // this wave's columns of z, contraction over tokens
-  V xv[TT];      // rows of x, unit 0
+  // operands that are read ahead of their chunk
+  V zv[UC];  // this wave's columns of z, contraction over tokens
+  V xv[TT];  // rows of x, unit 0
   auto fetch = [&](const char* buf) {
 #pragma unroll
-    for (int u = 0; u < UC; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        zv[u][n] = TZ::col(buf + Sh::kXY, u, g, i, F32 ? c0 / 4 + 4 * n : c0 / 8 + 2 * n, 0);
+    for (int u = 0; u < UC; ++u) zv[u] = TZ::col(buf + Sh::kXY, u, g, i, F32 ? c0 / 4 : c0 / 8, 0);
     if constexpr (!STATE) {
 #pragma unroll
       for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
@@ -559,51 +551,43 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);
   };
   // unit u of the state as an operand, 16 bit: in two terms
-  V zh[2][NT], zl[2][NT];
+  V zh[2], zl[2];
   auto state_operand = [&](int u) {
+    if constexpr (F32) {
+      zh[u & 1] = Z[u];
+    } else {
+      float x[8];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (F32) {
-        zh[u & 1][n] = Z[u][n];
-      } else {
-        float x[8];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][n][r], x[4 + r] = Z[2 * u + 1][n][r];
-        zh[u & 1][n] = pack_hi(x);
-        sub_hi(x);
-        zl[u & 1][n] = pack_rne(x);
-      }
+      for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][r], x[4 + r] = Z[2 * u + 1][r];
+      zh[u & 1] = pack_hi(x);
+      sub_hi(x);
+      zl[u & 1] = pack_rne(x);
     }
   };
   // c_j z_j of unit u, 16 bit: in SPLIT terms
   constexpr int TERMS = F32 ? 1 : SPLIT;
-  V zs[2][TERMS][NT];
+  V zs[2][TERMS];
   auto terms = [&](int u) {
+    if constexpr (F32) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (F32) {
+      for (int e = 0; e < 4; ++e) zs[u & 1][0][e] = cz[u][e] * zv[u][e];
+    } else {
+      float x[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) zs[u & 1][0][n][e] = cz[u][e] * zv[u][n][e];
-      } else {
-        float x[8];
+      for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][e]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][n][e]);
-#pragma unroll
-        for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
-          zs[u & 1][t2][n] = pack_hi(x);
-          sub_hi(x);
-        }
-        zs[u & 1][SPLIT - 1][n] = pack_rne(x);
+      for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
+        zs[u & 1][t2] = pack_hi(x);
+        sub_hi(x);
       }
+      zs[u & 1][SPLIT - 1] = pack_rne(x);
     }
   };
   auto decay = [&](int m0) {
 #pragma unroll
     for (int m = 0; m < MP; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) Z[m0 + m][n][r] *= gC;
+      for (int r = 0; r < 4; ++r) Z[m0 + m][r] *= gC;
   };
   // The barrier of a step. These waves write nothing to LDS, and what they have read ahead of it stays as it is for
   // two steps, so they need not wait for it.
@@ -612,6 +596,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  const bool want_last = STATE || (sw.Z1 != nullptr && t.seg + 1 == t.nseg);
   __syncthreads();
   if constexpr (!STATE) __syncthreads();
   int now = 0;  // this chunk's buffer
@@ -624,6 +609,7 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
     const char* const tp = scores + (s & 1) * Sh::kScores;
     const int valid = min(C, t.pos1 - (t.pos0 + s * C));
     const bool last = s + 1 == steps;
+    const int before = now;
     now = now == (STATE ? 1 : 2) ? 0 : now + 1;
     const char* const after = lds + now * BUF;
     if (valid < C) {
@@ -636,14 +622,12 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
         for (int m = 0; m < RT; ++m)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) Z[m][n][r] = fmaf(Z[m][n][r], rest, Z[m][n][r]);
+          for (int r = 0; r < 4; ++r) Z[m][r] = fmaf(Z[m][r], rest, Z[m][r]);
       }
     };
     V y[2][MP];
     // r^T from the state and from the scores: rows are columns of the state, columns are tokens
-    f32x4 R[TT][NT], R2[TT][NT];
+    f32x4 R[TT], R2[TT];
 
     if constexpr (!STATE) {
       // scores by unit: row tile k, unit u <= 16 k / KU
@@ -663,11 +647,9 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
           if constexpr (!F32) pl[n] = TP::row(tp + Sh::kP, 16 * k + i, u, g);
         });
       };
-      const int4 odd4 = *reinterpret_cast<const int4*>(flags + (now == 0 ? 2 : now - 1) * kLinLoad);
+      const int4 odd4 = *reinterpret_cast<const int4*>(flags + before * kLinLoad);
 #pragma unroll
-      for (int k = 0; k < TT; ++k)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) R[k][n] = R2[k][n] = zero4();
+      for (int k = 0; k < TT; ++k) R[k] = R2[k] = zero4();
 #pragma unroll
       for (int u = 0; u < UK; ++u) {
         V xn[TT];
@@ -678,17 +660,13 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
           get_scores(0, H1);
         }
 #pragma unroll
-        for (int k = 0; k < TT; ++k)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zh[u & 1][n], xv[k]);
+        for (int k = 0; k < TT; ++k) lin_mma(R[k], zh[u & 1], xv[k]);
         if constexpr (!F32) {
 #pragma unroll
-          for (int k = 0; k < TT; ++k)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) lin_mma(R[k][n], zl[u & 1][n], xv[k]);
+          for (int k = 0; k < TT; ++k) lin_mma(R[k], zl[u & 1], xv[k]);
         }
-        if (u + 1 < UK) state_operand(u + 1);  // beside the products
         if (u + 1 < UK) {
+          state_operand(u + 1);  // beside the products
 #pragma unroll
           for (int k = 0; k < TT; ++k) xv[k] = xn[k];
         }
@@ -697,28 +675,17 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       // a zero score times an infinity or NaN of a later token is NaN: such values of z are taken out of the product,
       // and added to their own and later tokens one by one
       const bool odd = __builtin_amdgcn_readfirstlane(odd4.x | odd4.y | odd4.z | odd4.w) != 0;
-      V zp[UC][NT];
+      V zp[UC];
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) zp[u][n] = zv[u][n];
+      for (int u = 0; u < UC; ++u) zp[u] = zv[u];
       if (odd) {
 #pragma unroll
-        for (int u = 0; u < UC; ++u)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) lin_finite(zp[u][n]);
+        for (int u = 0; u < UC; ++u) lin_finite(zp[u]);
       }
       make_up();
       auto add_scores = [&](int from, int to) {
-        if constexpr (!F32)
-          each_unit(from, to, [&](int n, int k, int u) {
-#pragma unroll
-            for (int c = 0; c < NT; ++c) lin_mma(R2[k][c], zp[u][c], pl[n]);
-          });
-        each_unit(from, to, [&](int n, int k, int u) {
-#pragma unroll
-          for (int c = 0; c < NT; ++c) lin_mma(R2[k][c], zp[u][c], ph[n]);
-        });
+        if constexpr (!F32) each_unit(from, to, [&](int n, int k, int u) { lin_mma(R2[k], zp[u], pl[n]); });
+        each_unit(from, to, [&](int n, int k, int u) { lin_mma(R2[k], zp[u], ph[n]); });
       };
       get_scores(H1, NU);
       add_scores(0, H1);
@@ -730,25 +697,23 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
       if (odd) {
 #pragma unroll
         for (int k = 0; k < TT; ++k)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
 #pragma unroll 1
-            for (int j = 0; j < 16 * (k + 1); ++j) {
-              float p;
-              if constexpr (F32) {
-                p = *reinterpret_cast<const float*>(tp + TP::at(16 * k + i, j >> 2) + 4 * (j & 3));
-              } else {
-                const char* at = tp + TP::at(16 * k + i, j >> 3) + 2 * (j & 7);
-                p = bf16_to_f32(*reinterpret_cast<const __bf16*>(at)) +
-                    bf16_to_f32(*reinterpret_cast<const __bf16*>(at + Sh::kP));
-              }
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int c = c0 + 16 * n + 4 * g + r;
-                const float z = load1<F32>(tz + TZ::at(j, c * ES / 16), c % (16 / ES));
-                if (j <= 16 * k + i && !(fabsf(z) <= 3.4028235e38f)) R2[k][n][r] += p * z;
-              }
+          for (int j = 0; j < 16 * (k + 1); ++j) {
+            float p;
+            if constexpr (F32) {
+              p = *reinterpret_cast<const float*>(tp + TP::at(16 * k + i, j >> 2) + 4 * (j & 3));
+            } else {
+              const char* at = tp + TP::at(16 * k + i, j >> 3) + 2 * (j & 7);
+              p = bf16_to_f32(*reinterpret_cast<const __bf16*>(at)) +
+                  bf16_to_f32(*reinterpret_cast<const __bf16*>(at + Sh::kP));
             }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int c = c0 + 4 * g + r;
+              const float z = load1<F32>(tz + TZ::at(j, c * ES / 16), c % (16 / ES));
+              if (j <= 16 * k + i && !(fabsf(z) <= 3.4028235e38f)) R2[k][r] += p * z;
+            }
+          }
       }
     } else {
 #pragma unroll
@@ -761,44 +726,37 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
       for (int k = 0; k < TT; ++k) {
         if (valid == C || 16 * k + i < valid) {
+          const int64_t at = rat + 16 * k * rstep;
+          f32x4 x;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int64_t at = rat + 16 * k * rstep + 16 * n;
-            f32x4 x;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = fmaf(R[k][n][r], ro[k], R2[k][n][r]);
-            if (F32 || sw.r_f32) st4(static_cast<float*>(sw.r) + at, x[0], x[1], x[2], x[3]);
-            else st4(static_cast<__bf16*>(sw.r) + at, x[0], x[1], x[2], x[3]);
-          }
+          for (int r = 0; r < 4; ++r) x[r] = fmaf(R[k][r], ro[k], R2[k][r]);
+          if (F32 || sw.r_f32) st4(static_cast<float*>(sw.r) + at, x[0], x[1], x[2], x[3]);
+          else st4(static_cast<__bf16*>(sw.r) + at, x[0], x[1], x[2], x[3]);
         }
       }
       rat += C * rstep;
     };
 
-    // Z <- g^n Z + sum_j y_j (c_j z_j)^T, for the last chunk too where nothing asks for it: a branch here would have the
-    // compiler move the terms above, which run beside the products of r, down into it
-    {
+    // Z <- g^n Z + sum_j y_j (c_j z_j)^T, for the last chunk too where nothing asks for it: a branch here would have
+    // the compiler move the terms above, which run beside the products of r, down into it
 #pragma unroll
-      for (int st = 0; st < NS; ++st) {
-        if (st + 1 < NS) {
+    for (int st = 0; st < NS; ++st) {
+      if (st + 1 < NS) {
 #pragma unroll
-          for (int m = 0; m < MP; ++m) y[(st + 1) & 1][m] = y_of(ty, st + 1, m);
-        }
-        const int u = st / SU, m0 = st % SU * MP;
-#pragma unroll
-        for (int t2 = TERMS - 1; t2 >= 0; --t2)
-#pragma unroll
-          for (int m = 0; m < MP; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) lin_mma(Z[m0 + m][n], y[st & 1][m], zs[u & 1][t2][n]);
-        // beside the products: the next stage's decay, the next unit's terms, the next chunk's first operand
-        if (st + 1 < SU) decay(m0 + MP);
-        if (st % SU == SU - 1 && u + 1 < UC) terms(u + 1);
-        if (!STATE && SU > 1 && st == NS - 1) state_operand(0);
-        if (!STATE && st == 0) store();
+        for (int m = 0; m < MP; ++m) y[(st + 1) & 1][m] = y_of(ty, st + 1, m);
       }
-      if (!STATE && SU == 1) state_operand(0);
+      const int u = st / SU, m0 = st % SU * MP;
+#pragma unroll
+      for (int t2 = TERMS - 1; t2 >= 0; --t2)
+#pragma unroll
+        for (int m = 0; m < MP; ++m) lin_mma(Z[m0 + m], y[st & 1][m], zs[u & 1][t2]);
+      // beside the products: the next stage's decay, the next unit's terms, the next chunk's first operand
+      if (st + 1 < SU) decay(m0 + MP);
+      if (st % SU == SU - 1 && u + 1 < UC) terms(u + 1);
+      if (!STATE && SU > 1 && st == NS - 1) state_operand(0);
+      if (!STATE && st == 0) store();
     }
+    if (!STATE && SU == 1) state_operand(0);
     if constexpr (!STATE) {  // the next chunk is in LDS since the step before
       if (!last) fetch(after);
       step_barrier();
@@ -814,12 +772,10 @@ __global__ __launch_bounds__((LinShape<A, NW, NT, F32>::kThreads), 2) void gdn2_
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = lin_state_row<F32>(m, g, r);
-          if (A >= KU || row < A) dst[(int64_t)row * E + e0 + 16 * n + i] = Z[m][n][r];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int row = lin_state_row<F32>(m, g, r);
+        if (A >= KU || row < A) dst[(int64_t)row * E + e0 + i] = Z[m][r];
+      }
   }
 }
 

@@ -5,11 +5,11 @@
 
 namespace gdn2 {
 
-template <int A, int NW, int NT, bool F32, bool STATE, int SPLIT>
+template <int A, int NW, bool F32, bool STATE, int SPLIT>
 static hipError_t launch_lin_s(const LinArgs& a, hipStream_t s) {
-  using Sh = LinShape<A, NW, NT, F32>;
+  using Sh = LinShape<A, NW, F32>;
   constexpr int lds = STATE ? Sh::kLdsState : Sh::kLds;
-  const auto kernel = gdn2_linattn_kernel<A, NW, NT, F32, STATE, SPLIT>;
+  const auto kernel = gdn2_linattn_kernel<A, NW, F32, STATE, SPLIT>;
   if (lds > 64 * 1024) {  // more than a launch takes without asking
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -23,23 +23,23 @@ static hipError_t launch_lin_s(const LinArgs& a, hipStream_t s) {
 
 // The decayed z of the update in three bf16 terms where a state can be an output (fp32 to its last bits), in two where
 // it only enters r, whose rounding to bf16 is 2^7 times what two terms leave.
-template <int A, int NW, int NT, bool F32, bool STATE>
+template <int A, int NW, bool F32, bool STATE>
 static hipError_t launch_lin_t(const LinArgs& a, hipStream_t s) {
   if constexpr (!F32) {
     bool exact = false;
     for (int i = 0; i < a.sweeps; ++i) exact |= a.sw[i].exact;
-    if (!exact) return launch_lin_s<A, NW, NT, F32, STATE, 2>(a, s);
+    if (!exact) return launch_lin_s<A, NW, F32, STATE, 2>(a, s);
   }
-  return launch_lin_s<A, NW, NT, F32, STATE, 3>(a, s);
+  return launch_lin_s<A, NW, F32, STATE, 3>(a, s);
 }
 
 template <int A, bool F32, bool STATE>
 static hipError_t launch_lin_e(const LinArgs& a, hipStream_t s) {
   switch (a.E) {
-    case 16: return launch_lin_t<A, 1, 1, F32, STATE>(a, s);
-    case 32: return launch_lin_t<A, 2, 1, F32, STATE>(a, s);
+    case 16: return launch_lin_t<A, 1, F32, STATE>(a, s);
+    case 32: return launch_lin_t<A, 2, F32, STATE>(a, s);
     case 64:
-    case 128: return launch_lin_t<A, 4, 1, F32, STATE>(a, s);
+    case 128: return launch_lin_t<A, 4, F32, STATE>(a, s);
   }
   return hipErrorInvalidValue;
 }
