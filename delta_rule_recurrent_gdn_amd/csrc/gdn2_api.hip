@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr int kVersion = 300;  // 0.3.0: the training pair (forward writes the backward records)
+constexpr int kVersion = 400;  // 0.4.0: linear attention with a decay for each head, q/k head norms with rotation
 constexpr unsigned kKnownFlags =
     GDN2_FLAG_RAW_GATES | GDN2_FLAG_SCALAR_B | GDN2_FLAG_SCALAR_W | GDN2_FLAG_SCALAR_DECAY;
 

@@ -1,7 +1,6 @@
 // gdn2_linattn_api.hip -- C entry points of the linear attention with a decay for each head and of the q/k head norms
 // with rotation: argument checks, workspace sizing, dispatch. No allocation, no host synchronisation, no state.
 
-#include <limits.h>
 #include <stdint.h>
 
 #include <initializer_list>
@@ -60,7 +59,8 @@ Plan plan(bool bwd, int N, int T, int Hk, int H, int Dk, int Dv, bool packed, in
   p.partial_bytes = bwd && H != Hk ? al256((size_t)(packed ? 1 : N) * T * H * Dk * 4) : 0;
   p.need = p.partial + 2 * p.partial_bytes;
   const int wide = (Dk > Dv ? Dk : Dv) <= 64 ? 1 : 2;
-  p.fits = slots * H * wide * sweeps < (size_t)INT_MAX - 64 && (size_t)N * H * 16 < (size_t)INT_MAX;
+  // a grid holds fewer than 2^32 threads: 512 a workgroup of the sweeps, 256 and up to 16 workgroups a state to join
+  p.fits = slots * H * wide * sweeps < ((size_t)1 << 23) - 64 && (size_t)N * H < (size_t)1 << 20;
   return p;
 }
 
@@ -187,7 +187,7 @@ int decode(const void* q, const void* k, const void* v, const float* log_decay, 
            int num_slots, void* o, int B, int Hk, int H, int Dk, int Dv, float scale, int dt, void* stream) {
   int st = check_sizes(B, 1, Hk, H, Dk, Dv, dt);
   if (st != GDN2_OK || B == 0 || H == 0) return st;
-  if ((int64_t)B * H > INT_MAX / 8) return GDN2_ERR_SHAPE;
+  if ((int64_t)B * H >= (int64_t)1 << 24) return GDN2_ERR_SHAPE;  // a grid holds fewer than 2^32 threads
   st = check_ptrs({q, k, v, S, o}, {});
   if (st == GDN2_OK && log_decay == nullptr) st = GDN2_ERR_NULL;
   if (st == GDN2_OK && (!aligned(log_decay, 4) || !aligned(slots, 4))) st = GDN2_ERR_ALIGN;
@@ -208,7 +208,7 @@ int norm_sizes(int64_t tokens, int64_t period, int Hq, int Hk, int D, int rot, f
   if (tokens < 0 || Hq < 1 || Hk < 0 || D < 0 || rot < 0 || rot > D) return GDN2_ERR_SHAPE;
   if (tokens > 0 && period < 1) return GDN2_ERR_SHAPE;
   if (!(eps >= 0.f)) return GDN2_ERR_SHAPE;
-  if ((int64_t)Hq + Hk > (1 << 20) || tokens > ((int64_t)1 << 31)) return GDN2_ERR_SHAPE;
+  if ((int64_t)Hq + Hk > (1 << 20) || tokens >= ((int64_t)1 << 26)) return GDN2_ERR_SHAPE;  // as above
   if (!dim_ok(D) || rot % 16 != 0) return GDN2_ERR_UNSUPPORTED;
   if ((flags & ~(GDN2_FLAG_L2_NORM | GDN2_FLAG_INTERLEAVED)) != 0) return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;

@@ -545,7 +545,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
     }
   };
-  constexpr int MP = RT >= 4 ? 4 : RT, SU = RT / MP, NS = UC * SU;  // tiles a stage of the update, stages a unit, in all
+  constexpr int MP = RT >= 4 ? 4 : RT, SU = RT / MP, NS = UC * SU;  // tiles a stage of the update, stages a unit, all
   auto y_of = [&](const char* ty, int st, int m) {                  // operand of stage st, its tile m
     const int u = st / SU, mt = st % SU * MP + m;
     return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);

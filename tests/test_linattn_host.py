@@ -62,7 +62,7 @@ def norm_bwd(**kw):
     (fwd, dict(k=A + 8), ALIGN), (fwd, dict(S0=A + 4), ALIGN), (fwd, dict(ld=A + 2), ALIGN),
     (fwd, dict(dt=2), DTYPE), (fwd, dict(Dk=48), UNSUPPORTED), (fwd, dict(Dv=256), UNSUPPORTED),
     (fwd, dict(H=3), SHAPE), (fwd, dict(Hk=0), SHAPE), (fwd, dict(T=-1), SHAPE), (fwd, dict(T=(1 << 30) + 1), SHAPE),
-    (fwd, dict(B=1 << 29, T=1), SHAPE),                      # more workgroups than a grid has
+    (fwd, dict(B=1 << 29, T=1), SHAPE), (fwd, dict(B=1 << 18, T=1), SHAPE),  # more threads than a grid holds
     (fwd, dict(T=65536), WORKSPACE), (fwd, dict(T=65536, ws=A, wsb=1), WORKSPACE),
     (fwd, dict(T=65536, ws=A + 16, wsb=1 << 40), ALIGN),
     (fwd, dict(B=0), OK), (fwd, dict(H=0), OK), (fwd, dict(T=0, q=None, o=None), OK),
@@ -74,13 +74,13 @@ def norm_bwd(**kw):
     (decode, dict(S=None), NULL), (decode, dict(slots=None), NULL), (decode, dict(num=-1), SHAPE),
     (decode, dict(S=A + 8), ALIGN), (decode, dict(slots=A + 2), ALIGN), (decode, dict(H=5), SHAPE),
     (decode, dict(Dk=80), UNSUPPORTED), (decode, dict(dt=9), DTYPE), (decode, dict(B=0), OK),
-    (decode, dict(B=1 << 28, Hk=4), SHAPE),
+    (decode, dict(B=1 << 22, Hk=4), SHAPE),
     (norm, dict(q=None), NULL), (norm, dict(k=None), NULL), (norm, dict(ko=None), NULL), (norm, dict(f=None), NULL),
     (norm, dict(q=A + 4), ALIGN), (norm, dict(pos=A + 4), ALIGN), (norm, dict(sq=132), ALIGN), (norm, dict(sq=64), SHAPE),
     (norm, dict(so=120), SHAPE), (norm, dict(rot=8), UNSUPPORTED), (norm, dict(rot=80), SHAPE),
     (norm, dict(rot=-16), SHAPE), (norm, dict(D=96), UNSUPPORTED), (norm, dict(flags=1), UNSUPPORTED),
     (norm, dict(eps=-1.0), SHAPE), (norm, dict(eps=float("nan")), SHAPE), (norm, dict(period=0), SHAPE),
-    (norm, dict(Hq=0), SHAPE), (norm, dict(n=-1), SHAPE), (norm, dict(dt=3), DTYPE), (norm, dict(n=0), OK),
+    (norm, dict(Hq=0), SHAPE), (norm, dict(n=-1), SHAPE), (norm, dict(n=1 << 26), SHAPE), (norm, dict(dt=3), DTYPE), (norm, dict(n=0), OK),
     (norm_bwd, dict(dq=None), NULL), (norm_bwd, dict(wq=A), WORKSPACE), (norm_bwd, dict(wq=A + 4), ALIGN),
     (norm_bwd, dict(wq=A, ws=A + 64, wsb=1 << 30), ALIGN), (norm_bwd, dict(dt=0, dtg=1), DTYPE),
     (norm_bwd, dict(sq=100), SHAPE), (norm_bwd, dict(n=0), OK),
