@@ -545,9 +545,9 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
     }
   };
-  constexpr int MP = RT >= 4 ? 4 : RT, SU = RT / MP, NS = UC * SU;  // tiles a stage of the update, stages a unit, all
-  auto y_of = [&](const char* ty, int st, int m) {                  // operand of stage st, its tile m
-    const int u = st / SU, mt = st % SU * MP + m;
+  constexpr int MP = RT >= 4 ? 4 : RT, NS = UC * (RT / MP);  // state tiles a stage of the update, stages (units within tiles)
+  auto y_of = [&](const char* ty, int st, int m) {           // operand of stage st, its tile m
+    const int u = st % UC, mt = st / UC * MP + m;
     return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);
   };
   // unit u of the state as an operand, 16 bit: in two terms
@@ -566,28 +566,22 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
   };
   // c_j z_j of unit u, 16 bit: in SPLIT terms
   constexpr int TERMS = F32 ? 1 : SPLIT;
-  V zs[2][TERMS];
+  V zs[UC][TERMS];
   auto terms = [&](int u) {
     if constexpr (F32) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) zs[u & 1][0][e] = cz[u][e] * zv[u][e];
+      for (int e = 0; e < 4; ++e) zs[u][0][e] = cz[u][e] * zv[u][e];
     } else {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][e]);
 #pragma unroll
       for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
-        zs[u & 1][t2] = pack_hi(x);
+        zs[u][t2] = pack_hi(x);
         sub_hi(x);
       }
-      zs[u & 1][SPLIT - 1] = pack_rne(x);
+      zs[u][SPLIT - 1] = pack_rne(x);
     }
-  };
-  auto decay = [&](int m0) {
-#pragma unroll
-    for (int m = 0; m < MP; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) Z[m0 + m][r] *= gC;
   };
   // The barrier of a step. These waves write nothing to LDS, and what they have read ahead of it stays as it is for
   // two steps, so they need not wait for it.
@@ -693,7 +687,6 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
 #pragma unroll
       for (int m = 0; m < MP; ++m) y[0][m] = y_of(ty, 0, m);
       add_scores(H1, NU);
-      decay(0);
       if (odd) {
 #pragma unroll
         for (int k = 0; k < TT; ++k)
@@ -720,7 +713,6 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       for (int m = 0; m < MP; ++m) y[0][m] = y_of(ty, 0, m);
       make_up();
       terms(0);
-      decay(0);
     }
     auto store = [&] {
 #pragma unroll
@@ -737,26 +729,43 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       rat += C * rstep;
     };
 
-    // Z <- g^n Z + sum_j y_j (c_j z_j)^T, for the last chunk too where nothing asks for it: a branch here would have
-    // the compiler move the terms above, which run beside the products of r, down into it
+    // Z <- g^n Z + sum_j y_j (c_j z_j)^T. Where the state can be an output, the chunk's sum apart: one rounding a chunk in
+    // a state that is carried over thousands (64K tokens of hardly any decay: 3.3e-7 off, 1.2e-6 with every product
+    // added to the state itself; 3 % of the time). For the last chunk too where nothing asks for it: a branch here
+    // would have the compiler move the terms above, which run beside the products of r, down into it
+    constexpr bool APART = F32 || SPLIT == 3;
+    f32x4 T[MP];
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
       if (st + 1 < NS) {
 #pragma unroll
         for (int m = 0; m < MP; ++m) y[(st + 1) & 1][m] = y_of(ty, st + 1, m);
       }
-      const int u = st / SU, m0 = st % SU * MP;
+      const int u = st % UC, m0 = st / UC * MP;
+      if (u == 0) {
+#pragma unroll
+        for (int m = 0; m < MP; ++m) {
+          T[m] = zero4();
+          if constexpr (!APART) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) T[m][r] = Z[m0 + m][r] * gC;
+          }
+        }
+      }
 #pragma unroll
       for (int t2 = TERMS - 1; t2 >= 0; --t2)
 #pragma unroll
-        for (int m = 0; m < MP; ++m) lin_mma(Z[m0 + m], y[st & 1][m], zs[u & 1][t2]);
-      // beside the products: the next stage's decay, the next unit's terms, the next chunk's first operand
-      if (st + 1 < SU) decay(m0 + MP);
-      if (st % SU == SU - 1 && u + 1 < UC) terms(u + 1);
-      if (!STATE && SU > 1 && st == NS - 1) state_operand(0);
+        for (int m = 0; m < MP; ++m) lin_mma(T[m], y[st & 1][m], zs[u][t2]);
+      if (st + 1 < UC) terms(st + 1);  // beside the products
+      if (u == UC - 1) {
+#pragma unroll
+        for (int m = 0; m < MP; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) Z[m0 + m][r] = APART ? fmaf(Z[m0 + m][r], gC, T[m][r]) : T[m][r];
+      }
       if (!STATE && st == 0) store();
     }
-    if (!STATE && SU == 1) state_operand(0);
+    if (!STATE) state_operand(0);
     if constexpr (!STATE) {  // the next chunk is in LDS since the step before
       if (!last) fetch(after);
       step_barrier();

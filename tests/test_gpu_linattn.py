@@ -355,6 +355,27 @@ def test_decode_many_entries(Dk, Dv):
         assert ((S - (old + new)).abs() <= 4 * 2.0 ** -24 * (old.abs() + new.abs())).all()
 
 
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "fp32"])
+def test_state_over_a_long_slow_decay(dt):
+    """The state of 8192 tokens walked by one workgroup, hardly decaying: a chunk's sum is added with one rounding (rms
+    below 2^-24 / sqrt(3) of the value), so over n chunks the norm of the error stays below sqrt(n) 2^-24."""
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    B, T, H, Dk, Dv = 64, 8192, 4, 32, 16
+    assert gdn.gdn2_linattn_workspace_bytes(0, B, T, H, H, Dk, Dv, dt) == 0
+    g = torch.Generator(device="cuda").manual_seed(40)
+    k, v = (torch.randn(B, T, H, d, generator=g, device="cuda").to(dt) for d in (Dk, Dv))
+    ld = torch.tensor([0.0, -2.0 ** -15, -2.0 ** -12, -2.0 ** -9], device="cuda")
+    _, S = gdn.gdn2_linattn_fwd_chunked(k, k, v, ld)
+    weight = torch.exp(ld.double() * torch.arange(T - 1, -1, -1, device="cuda", dtype=torch.float64)[:, None])
+    kd, vd = (k.double() * weight[None, :, :, None]).permute(0, 2, 3, 1).contiguous(), v.double().transpose(1, 2).contiguous()
+    want = torch.matmul(kd, vd)
+    n = T // (64 if dt == BF16 else 32)
+    for h in range(H):
+        off = (S[:, h].double() - want[:, h]).norm() / want[:, h].norm()
+        assert off <= n ** 0.5 * 2.0 ** -24, (h, float(off))
+
+
 def test_deterministic_and_on_a_side_stream():
     import delta_rule_recurrent_gdn_amd as gdn
 
