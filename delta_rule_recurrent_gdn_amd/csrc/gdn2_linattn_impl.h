@@ -19,6 +19,14 @@
 // that x is read in from LDS with one 16-byte access, so the state enters its product from the registers it is
 // kept in. The contraction over tokens reads y and z column-wise with the transposing LDS read (16 bit).
 //
+// What bounds it (B8 H16 T4096 d128 bf16, 256 workgroups, one a CU): 159-165 us by card, 3.4 TB/s of the 0.54 GB that
+// it has to read and write, once each by the counters (a copy: 5.2 TB/s, 105 us). The loads alone take 98 us, the
+// state's waves with their data at hand 126: with one workgroup a CU and a barrier a chunk the two cover each other in
+// part. Of the SIMDs' time vector instructions take 39 %, the matrix cores 27 %; LDS is busy for 32 %, and its
+// conflicts are not what is waited for. So the work is split by role: the state's waves never wait for memory (249 us
+// with one role, 161 with loading waves that also form the scores). 64K tokens of one sequence: 442-468 us, 2.4 TB/s
+// of 1.07 GB: y and z are read a second time, for the pieces' states.
+//
 // Precision (16-bit inputs): products of two inputs are exact in the matrix cores' fp32 sums. The decayed z is
 // split into three bf16 terms, the state as an operand and the scores into two, so that r is rounded once, at the
 // end, and the states are fp32 sums of unrounded products.
@@ -545,7 +553,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       for (int k = 0; k < TT; ++k) xv[k] = TX::row(buf + Sh::kBuf, 16 * k + i, 0, g);
     }
   };
-  constexpr int MP = RT >= 4 ? 4 : RT, NS = UC * (RT / MP);  // state tiles a stage of the update, stages (units within tiles)
+  constexpr int MP = RT >= 4 ? 4 : RT, NS = UC * (RT / MP);  // state tiles a stage of the update; stages, units fastest
   auto y_of = [&](const char* ty, int st, int m) {           // operand of stage st, its tile m
     const int u = st % UC, mt = st / UC * MP + m;
     return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);
@@ -584,8 +592,10 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
     }
   };
   // The barrier of a step. These waves write nothing to LDS, and what they have read ahead of it stays as it is for
-  // two steps, so they need not wait for it.
+  // two steps, so they need not wait for it. What they read of this step's buffers is in the products that come before
+  // (and stay before, at 1 % of the time: the loading waves write those buffers after the barrier).
   auto step_barrier = [] {
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -729,10 +739,10 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       rat += C * rstep;
     };
 
-    // Z <- g^n Z + sum_j y_j (c_j z_j)^T. Where the state can be an output, the chunk's sum apart: one rounding a chunk in
-    // a state that is carried over thousands (64K tokens of hardly any decay: 3.3e-7 off, 1.2e-6 with every product
-    // added to the state itself; 3 % of the time). For the last chunk too where nothing asks for it: a branch here
-    // would have the compiler move the terms above, which run beside the products of r, down into it
+    // Z <- g^n Z + sum_j y_j (c_j z_j)^T. Where the state can be an output, the chunk's sum apart: one rounding a
+    // chunk in a state that is carried over thousands (64K tokens of hardly any decay: 3.3e-7 off, 1.2e-6 with every
+    // product added to the state itself; 3 % of the time). For the last chunk too where nothing asks for it: a branch
+    // here would have the compiler move the terms above, which run beside the products of r, down into it
     constexpr bool APART = F32 || SPLIT == 3;
     f32x4 T[MP];
 #pragma unroll

@@ -393,7 +393,9 @@ int gdn2_fwd_chunked_noalloc(const void* q, const void* k, const void* v, const 
  *   and head, with its gradient, is gdn2_fwd_chunked_ex's GDN2_FLAG_SCALAR_DECAY).
  * - An infinity or NaN in a token never reaches an earlier token's output (of gradients: dq's; a later token's dk
  *   and dv), nor another sequence's; the state it enters is not finite from there on.
- * - Deterministic, asynchronous on `stream`, no allocation; the general conventions above.
+ * - Deterministic, asynchronous on `stream`, no allocation; the general conventions above. With bf16 inputs the
+ *   backward keeps 2^-16 of each term of its states where dS0 is not asked for, all of it where it is: dq, dk, dv may
+ *   differ in their last bit between the two.
  *   S0, S_final, dS_final, dS0 are nullable; S_final may be S0, and dS0 may be S0 or dS_final.
  *   workspace: gdn2_linattn_workspace_bytes(...) bytes, 256-byte aligned (may be NULL where that is 0); calls that
  *   may overlap need one each.
@@ -445,7 +447,8 @@ int gdn2_linattn_decode_step_slots(const void* q, const void* k, const void* v, 
  *   strides multiples of 16 bytes and at least a row. D in {16, 32, 64, 128}; rot a multiple of 16, 0 <= rot <= D.
  * - q_weight, k_weight [D] fp32, nullable (ones); inv_freq [rot/2] fp32.
  * - positions int64: row n has positions[n % period] (period = T for positions shared by a batch's rows, else
- *   tokens); NULL: n % period. Any int64 value; the angle is reduced in fp64, so far positions lose nothing.
+ *   tokens); NULL: n % period. Any int64 value; the angle is formed and reduced in fp64 (off by at most its size
+ *   times 2^-52, so positions to 2^27 lose nothing of fp32).
  *
  * gdn2_qk_norm_rope_bwd: from dq_out, dk_out (contiguous rows, type dt_grad: dt, or GDN2_F32 as the mixers'
  * backward gives) the gradients dq, dk (type dt, rows q_grad_stride, k_grad_stride apart: the fused projection's
