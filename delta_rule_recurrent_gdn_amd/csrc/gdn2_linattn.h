@@ -22,7 +22,6 @@ struct LinSweep {
   bool r_f32;
   bool rev;                      // walk every sequence from its last token to its first
   int first;                     // 1: the entering state is decayed once before the first token, 0: not
-  bool exact;                    // the sweep's state can be an output: fp32 to its last bits
   float si, so;                  // scale of y z^T, scale of r
   const float* Z0;               // entering states [N, H, ...], nullable; element (a, e) at a * z0_rs + e * z0_cs
   int z0_rs, z0_cs;

@@ -118,7 +118,7 @@ int forward(const Call& c, void* o, float* S_final) {
   const int G = c.H / c.Hk;
   a.A = c.Dk;
   a.E = c.Dv;
-  a.sw[0] = gdn2::LinSweep{c.q, c.k, c.v, o, G, G, 1, false, false, 1, true, 1.f, c.scale, c.S0, c.Dv, 1, S_final,
+  a.sw[0] = gdn2::LinSweep{c.q, c.k, c.v, o, G, G, 1, false, false, 1, 1.f, c.scale, c.S0, c.Dv, 1, S_final,
                            reinterpret_cast<float*>(c.ws + p.states)};
   a.sweeps = 1;
   return hip_status(gdn2::launch_linattn_sweeps(a, c.stream));
@@ -147,13 +147,13 @@ int backward(const Call& c, const void* dO, const float* dS_final, void* dq, voi
   void* const dq_to = G == 1 ? dq : at(p.partial);
   void* const dk_to = G == 1 ? dk : at(p.partial + p.partial_bytes);
   // dq: the forward recurrence of S^T, over (dO, v, k)
-  const gdn2::LinSweep sq{dO, c.v, c.k, dq_to, 1, 1, G, G > 1, false, 1, false, 1.f, c.scale,
+  const gdn2::LinSweep sq{dO, c.v, c.k, dq_to, 1, 1, G, G > 1, false, 1, 1.f, c.scale,
                           c.S0, 1, c.Dv, nullptr, at(p.states)};
   // dk: the reversed recurrence of the state's gradient, transposed, over (v, dO, q)
-  const gdn2::LinSweep sk{c.v, dO, c.q, dk_to, 1, 1, G, G > 1, true, 0, false, c.scale, 1.f,
+  const gdn2::LinSweep sk{c.v, dO, c.q, dk_to, 1, 1, G, G > 1, true, 0, c.scale, 1.f,
                           dS_final, 1, c.Dv, nullptr, at(p.states + p.state_bytes)};
   // dv: the same state, over (k, q, dO); its last value is dS0
-  const gdn2::LinSweep sv{c.k, c.q, dO, dv, G, G, 1, false, true, 0, dS0 != nullptr, c.scale, 1.f,
+  const gdn2::LinSweep sv{c.k, c.q, dO, dv, G, G, 1, false, true, 0, c.scale, 1.f,
                           dS_final, c.Dv, 1, dS0, at(p.states + 2 * p.state_bytes)};
   hipError_t e = hipSuccess;
   // dS0 may be S0 or dS_final: with pieces all entering states are read before the last are written, else they are
@@ -165,7 +165,6 @@ int backward(const Call& c, const void* dO, const float* dS_final, void* dq, voi
   a.sw[1] = sk;
   a.sw[2] = sv;
   a.sweeps = c.Dk == c.Dv && !apart ? 3 : 2;
-  a.sw[0].exact = apart && c.Dk == c.Dv;  // as in one launch with dS0's: the same bits either way
   e = gdn2::launch_linattn_sweeps(a, c.stream);
   if (e == hipSuccess && a.sweeps == 2) {
     a.A = c.Dk;

@@ -27,9 +27,9 @@
 // with one role, 161 with loading waves that also form the scores). 64K tokens of one sequence: 442-468 us, 2.4 TB/s
 // of 1.07 GB: y and z are read a second time, for the pieces' states.
 //
-// Precision (16-bit inputs): products of two inputs are exact in the matrix cores' fp32 sums. The decayed z is
-// split into three bf16 terms, the state as an operand and the scores into two, so that r is rounded once, at the
-// end, and the states are fp32 sums of unrounded products.
+// Precision (16-bit inputs): products of two inputs are exact in the matrix cores' fp32 sums. The scores, the decayed
+// z and the state as an operand are split into three bf16 terms each, which hold an fp32 value's 24 bits: r and the
+// states are fp32 sums of unrounded products, and r is rounded once, at the end.
 #pragma once
 
 #include <type_traits>
@@ -197,11 +197,13 @@ __device__ __forceinline__ void sub_hi(float (&x)[8]) {           // what trunca
 #pragma unroll
   for (int j = 0; j < 8; ++j) x[j] -= __uint_as_float(__float_as_uint(x[j]) & 0xffff0000u);
 }
-__device__ __forceinline__ bf16x8 pack_rne(const float (&x)[8]) {
-  bf16x8 b;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = f32_to_bf16(x[j]);
-  return b;
+// x in three bf16 terms, the largest first: 8 bits of it each, all of it together. x is used up.
+__device__ __forceinline__ void lin_split(float (&x)[8], bf16x8 (&t)[3]) {
+  t[0] = pack_hi(x);
+  sub_hi(x);
+  t[1] = pack_hi(x);
+  sub_hi(x);
+  t[2] = pack_hi(x);
 }
 
 // infinities and NaN replaced by zeros
@@ -232,10 +234,11 @@ struct LinShape {
   static constexpr int kP = Op::C * Op::C * Op::ES;
   static constexpr int kThreads = 64 * (NW + kLinLoad);
   static constexpr int kBuf = kXY + kZ, kBufX = 2 * kXY + kZ;  // y, z; y, z, x
-  static constexpr int kScores = (F32 ? 1 : 2) * kP;
+  static constexpr int kScores = F32 ? kP : 2 * kP + kP / 4;
   // three buffers of a chunk's rows, two of its scores, flags; the sums of the pieces: two buffers
   static constexpr int kLds = 3 * kBufX + 2 * kScores + 3 * 4 * kLinLoad;
   static constexpr int kLdsState = 2 * kBuf;
+  static_assert(kLds <= 160 * 1024, "a CU's LDS");
 };
 
 // What a workgroup has to do. Returns false where there is nothing.
@@ -243,6 +246,23 @@ struct LinTask {
   int n, h, seg, nseg, slot;
   int64_t tok0;    // row of the walk's first token
   int len, pos0, pos1;
+};
+
+// The scores of a chunk in LDS, 16 bit: a tile for the first terms, one for the second. Tokens of the first half of a
+// chunk have no scores with the second half's, so a quarter of each tile is free: the third terms of the first half's
+// rows lie in the first tile's, those of the second half's rows with the first half's tokens in the second tile's, the
+// rest in a tile of their own (three whole tiles, twice, would not fit beside the rows).
+struct LinScores {
+  static constexpr int C = LinOp<false>::C, kTile = C * C * 2;
+  using T = LinTile<false, C, kRows>;
+  using Rest = LinTile<false, C / 2, kRows>;
+  // byte offset of term n of block b of row r
+  __device__ __forceinline__ static int at(int n, int r, int b) {
+    constexpr int H = C / 2, HB = C / 16;  // half a chunk: rows, blocks
+    if (n < 2) return n * kTile + T::at(r, b);
+    if (r < H) return T::at(r, b + HB);
+    return b < HB ? kTile + T::at(r - H, b + HB) : 2 * kTile + Rest::at(r - H, b - HB);
+  }
 };
 
 __device__ __forceinline__ bool lin_task(const LinArgs& a, int item, bool rev, LinTask& t) {
@@ -370,19 +390,18 @@ struct LinLoader {
       if constexpr (F32) {
         *reinterpret_cast<f32x4*>(tp + TP::at(16 * ts + i, 4 * jt + g)) = p;
       } else {
-        bf16x4 hi, lo;
+        // in three terms; a unit has 32 tokens: zeros in the tile past the diagonal of an even strip
+        const int row = 16 * ts + i, half = 8 * (g & 1);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          hi[r] = f32_to_bf16(p[r]);
-          lo[r] = f32_to_bf16(p[r] - bf16_to_f32(hi[r]));
-        }
-        const int at = TP::at(16 * ts + i, 2 * jt + (g >> 1)) + 8 * (g & 1);
-        *reinterpret_cast<bf16x4*>(tp + at) = hi;
-        *reinterpret_cast<bf16x4*>(tp + Sh::kP + at) = lo;
-        if (ts == jt && (ts & 1) == 0) {  // a unit of 32 tokens: the tile past the diagonal of an even strip
-          const int past = TP::at(16 * ts + i, 2 * (ts + 1) + (g >> 1)) + 8 * (g & 1);
-          *reinterpret_cast<uint2*>(tp + past) = make_uint2(0u, 0u);
-          *reinterpret_cast<uint2*>(tp + Sh::kP + past) = make_uint2(0u, 0u);
+        for (int t2 = 0; t2 < 3; ++t2) {
+          uint2 w;
+          w.x = __builtin_amdgcn_perm(__float_as_uint(p[1]), __float_as_uint(p[0]), 0x07060302u);
+          w.y = __builtin_amdgcn_perm(__float_as_uint(p[3]), __float_as_uint(p[2]), 0x07060302u);
+          *reinterpret_cast<uint2*>(tp + LinScores::at(t2, row, 2 * jt + (g >> 1)) + half) = w;
+          if (ts == jt && (ts & 1) == 0)
+            *reinterpret_cast<uint2*>(tp + LinScores::at(t2, row, 2 * (ts + 1) + (g >> 1)) + half) = make_uint2(0u, 0u);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[r] -= __uint_as_float(__float_as_uint(p[r]) & 0xffff0000u);
         }
       }
     }
@@ -396,7 +415,7 @@ struct LinLoader {
 // chunk s, they write chunk s + 2 to LDS, send for chunk s + 3 and form the scores of chunk s + 1 (which do not depend
 // on the state), with one barrier a step; in this order the rows are on their way while the scores are formed (161 us
 // against 167 for a B8 H16 T4096 d128 forward). (STATE: no scores, chunk s + 1 to LDS, s + 2 sent for.)
-template <int A, int NW, bool F32, bool STATE, int SPLIT>
+template <int A, int NW, bool F32, bool STATE>
 __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_linattn_kernel(LinArgs a) {
   using Sh = LinShape<A, NW, F32>;
   using Op = LinOp<F32>;
@@ -410,7 +429,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
   using TP = LinTile<F32, C, kRows>;
 
   extern __shared__ char lds[];  // a buffer: y, z, x
-  char* const scores = lds + 3 * BUF;  // scores, then (16 bit) what their first bf16 term leaves
+  char* const scores = lds + 3 * BUF;  // two buffers
   int* const flags = reinterpret_cast<int*>(scores + 2 * Sh::kScores);  // [3][kLinLoad]: z has an infinity or NaN
 
   const int ncg = (a.E + CW - 1) / CW;
@@ -558,22 +577,20 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
     const int u = st % UC, mt = st / UC * MP + m;
     return F32 ? TY::col(ty, u, g, i, 4 * mt, 0) : TY::col(ty, u, g, i, 4 * (mt >> 1), mt & 1);
   };
-  // unit u of the state as an operand, 16 bit: in two terms
-  V zh[2], zl[2];
+  constexpr int TERMS = F32 ? 1 : 3;  // of the state, the scores and c_j z_j as operands
+  // unit u of the state as an operand
+  V zo[2][TERMS];
   auto state_operand = [&](int u) {
     if constexpr (F32) {
-      zh[u & 1] = Z[u];
+      zo[u & 1][0] = Z[u];
     } else {
       float x[8];
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] = Z[2 * u][r], x[4 + r] = Z[2 * u + 1][r];
-      zh[u & 1] = pack_hi(x);
-      sub_hi(x);
-      zl[u & 1] = pack_rne(x);
+      lin_split(x, zo[u & 1]);
     }
   };
-  // c_j z_j of unit u, 16 bit: in SPLIT terms
-  constexpr int TERMS = F32 ? 1 : SPLIT;
+  // c_j z_j of unit u
   V zs[UC][TERMS];
   auto terms = [&](int u) {
     if constexpr (F32) {
@@ -583,12 +600,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = cz[u][e] * bf16_to_f32(zv[u][e]);
-#pragma unroll
-      for (int t2 = 0; t2 + 1 < SPLIT; ++t2) {
-        zs[u][t2] = pack_hi(x);
-        sub_hi(x);
-      }
-      zs[u][SPLIT - 1] = pack_rne(x);
+      lin_split(x, zs[u]);
     }
   };
   // The barrier of a step. These waves write nothing to LDS, and what they have read ahead of it stays as it is for
@@ -636,7 +648,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
     if constexpr (!STATE) {
       // scores by unit: row tile k, unit u <= 16 k / KU
       constexpr int NU = F32 ? TT * (TT + 1) / 2 : TT * (TT + 2) / 4, H1 = NU / 2;
-      V ph[NU], pl[F32 ? 1 : NU];
+      V ps[NU][TERMS];
       auto each_unit = [&](int from, int to, auto f) {
         int n = 0;
 #pragma unroll
@@ -647,8 +659,13 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       };
       auto get_scores = [&](int from, int to) {
         each_unit(from, to, [&](int n, int k, int u) {
-          ph[n] = TP::row(tp, 16 * k + i, u, g);
-          if constexpr (!F32) pl[n] = TP::row(tp + Sh::kP, 16 * k + i, u, g);
+          if constexpr (F32) {
+            ps[n][0] = TP::row(tp, 16 * k + i, u, g);
+          } else {
+#pragma unroll
+            for (int t2 = 0; t2 < TERMS; ++t2)
+              ps[n][t2] = *reinterpret_cast<const V*>(tp + LinScores::at(t2, 16 * k + i, 4 * u + g));
+          }
         });
       };
       const int4 odd4 = *reinterpret_cast<const int4*>(flags + before * kLinLoad);
@@ -664,11 +681,9 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
           get_scores(0, H1);
         }
 #pragma unroll
-        for (int k = 0; k < TT; ++k) lin_mma(R[k], zh[u & 1], xv[k]);
-        if constexpr (!F32) {
+        for (int t2 = TERMS - 1; t2 >= 0; --t2)
 #pragma unroll
-          for (int k = 0; k < TT; ++k) lin_mma(R[k], zl[u & 1], xv[k]);
-        }
+          for (int k = 0; k < TT; ++k) lin_mma(R[k], zo[u & 1][t2], xv[k]);
         if (u + 1 < UK) {
           state_operand(u + 1);  // beside the products
 #pragma unroll
@@ -688,8 +703,9 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       }
       make_up();
       auto add_scores = [&](int from, int to) {
-        if constexpr (!F32) each_unit(from, to, [&](int n, int k, int u) { lin_mma(R2[k], zp[u], pl[n]); });
-        each_unit(from, to, [&](int n, int k, int u) { lin_mma(R2[k], zp[u], ph[n]); });
+#pragma unroll
+        for (int t2 = TERMS - 1; t2 >= 0; --t2)
+          each_unit(from, to, [&](int n, int k, int u) { lin_mma(R2[k], zp[u], ps[n][t2]); });
       };
       get_scores(H1, NU);
       add_scores(0, H1);
@@ -706,9 +722,10 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
             if constexpr (F32) {
               p = *reinterpret_cast<const float*>(tp + TP::at(16 * k + i, j >> 2) + 4 * (j & 3));
             } else {
-              const char* at = tp + TP::at(16 * k + i, j >> 3) + 2 * (j & 7);
-              p = bf16_to_f32(*reinterpret_cast<const __bf16*>(at)) +
-                  bf16_to_f32(*reinterpret_cast<const __bf16*>(at + Sh::kP));
+              const auto term = [&](int n) {
+                return bf16_to_f32(*reinterpret_cast<const __bf16*>(tp + LinScores::at(n, 16 * k + i, j >> 3) + 2 * (j & 7)));
+              };
+              p = term(0) + (term(1) + term(2));
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -739,11 +756,8 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       rat += C * rstep;
     };
 
-    // Z <- g^n Z + sum_j y_j (c_j z_j)^T. Where the state can be an output, the chunk's sum apart: one rounding a
-    // chunk in a state that is carried over thousands (64K tokens of hardly any decay: 3.3e-7 off, 1.2e-6 with every
-    // product added to the state itself; 3 % of the time). For the last chunk too where nothing asks for it: a branch
-    // here would have the compiler move the terms above, which run beside the products of r, down into it
-    constexpr bool APART = F32 || SPLIT == 3;
+    // Z <- g^n Z + sum_j y_j (c_j z_j)^T, the chunk's sum apart: one rounding a chunk in a state that is carried over
+    // thousands (64K tokens of hardly any decay: 3.3e-7 off, 1.2e-6 with every product added to the state itself)
     f32x4 T[MP];
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
@@ -754,13 +768,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
       const int u = st % UC, m0 = st / UC * MP;
       if (u == 0) {
 #pragma unroll
-        for (int m = 0; m < MP; ++m) {
-          T[m] = zero4();
-          if constexpr (!APART) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) T[m][r] = Z[m0 + m][r] * gC;
-          }
-        }
+        for (int m = 0; m < MP; ++m) T[m] = zero4();
       }
 #pragma unroll
       for (int t2 = TERMS - 1; t2 >= 0; --t2)
@@ -771,7 +779,7 @@ __global__ __launch_bounds__((LinShape<A, NW, F32>::kThreads), 2) void gdn2_lina
 #pragma unroll
         for (int m = 0; m < MP; ++m)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) Z[m0 + m][r] = APART ? fmaf(Z[m0 + m][r], gC, T[m][r]) : T[m][r];
+          for (int r = 0; r < 4; ++r) Z[m0 + m][r] = fmaf(Z[m0 + m][r], gC, T[m][r]);
       }
       if (!STATE && st == 0) store();
     }

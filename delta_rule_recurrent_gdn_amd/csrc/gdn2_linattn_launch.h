@@ -5,11 +5,11 @@
 
 namespace gdn2 {
 
-template <int A, int NW, bool F32, bool STATE, int SPLIT>
-static hipError_t launch_lin_s(const LinArgs& a, hipStream_t s) {
+template <int A, int NW, bool F32, bool STATE>
+static hipError_t launch_lin_t(const LinArgs& a, hipStream_t s) {
   using Sh = LinShape<A, NW, F32>;
   constexpr int lds = STATE ? Sh::kLdsState : Sh::kLds;
-  const auto kernel = gdn2_linattn_kernel<A, NW, F32, STATE, SPLIT>;
+  const auto kernel = gdn2_linattn_kernel<A, NW, F32, STATE>;
   if (lds > 64 * 1024) {  // more than a launch takes without asking
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -19,18 +19,6 @@ static hipError_t launch_lin_s(const LinArgs& a, hipStream_t s) {
   const int64_t blocks = (items + 7) / 8 * 8 * ((a.E + Sh::CW - 1) / Sh::CW) * a.sweeps;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(Sh::kThreads), lds, s, a);
   return hipGetLastError();
-}
-
-// The decayed z of the update in three bf16 terms where a state can be an output (fp32 to its last bits), in two where
-// it only enters r, whose rounding to bf16 is 2^7 times what two terms leave.
-template <int A, int NW, bool F32, bool STATE>
-static hipError_t launch_lin_t(const LinArgs& a, hipStream_t s) {
-  if constexpr (!F32) {
-    bool exact = false;
-    for (int i = 0; i < a.sweeps; ++i) exact |= a.sw[i].exact;
-    if (!exact) return launch_lin_s<A, NW, F32, STATE, 2>(a, s);
-  }
-  return launch_lin_s<A, NW, F32, STATE, 3>(a, s);
 }
 
 template <int A, bool F32, bool STATE>

@@ -393,9 +393,8 @@ int gdn2_fwd_chunked_noalloc(const void* q, const void* k, const void* v, const 
  *   and head, with its gradient, is gdn2_fwd_chunked_ex's GDN2_FLAG_SCALAR_DECAY).
  * - An infinity or NaN in a token never reaches an earlier token's output (of gradients: dq's; a later token's dk
  *   and dv), nor another sequence's; the state it enters is not finite from there on.
- * - Deterministic, asynchronous on `stream`, no allocation; the general conventions above. With bf16 inputs the
- *   backward keeps 2^-16 of each term of its states where dS0 is not asked for, all of it where it is: dq, dk, dv may
- *   differ in their last bit between the two.
+ * - Deterministic, asynchronous on `stream`, no allocation; the general conventions above. Scores, states and sums
+ *   have fp32's 24 bits throughout, with bf16 inputs too; only the outputs are rounded to bf16.
  *   S0, S_final, dS_final, dS0 are nullable; S_final may be S0, and dS0 may be S0 or dS_final.
  *   workspace: gdn2_linattn_workspace_bytes(...) bytes, 256-byte aligned (may be NULL where that is 0); calls that
  *   may overlap need one each.
