@@ -58,12 +58,16 @@ __global__ __launch_bounds__((LinDecodeShape<DK, DV>::kThreads)) void gdn2_linat
     q[i] = load1<F32>(a.q, qk + rg + RG * i);
     k[i] = load1<F32>(a.k, qk + rg + RG * i);
   }
-  const float g = expf(a.log_decay[h]);
+  // the decay and what rounding left of it: a state is multiplied by it at every token, always off to the same side
+  const double decay = exp((double)a.log_decay[h]);
+  const float g = (float)decay, rest = g <= 3.4028235e38f ? (float)(decay - g) : 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    s[i].x = fmaf(g, s[i].x, k[i] * v[0]); s[i].y = fmaf(g, s[i].y, k[i] * v[1]);
-    s[i].z = fmaf(g, s[i].z, k[i] * v[2]); s[i].w = fmaf(g, s[i].w, k[i] * v[3]);
+    s[i].x = fmaf(g, s[i].x, fmaf(rest, s[i].x, k[i] * v[0]));
+    s[i].y = fmaf(g, s[i].y, fmaf(rest, s[i].y, k[i] * v[1]));
+    s[i].z = fmaf(g, s[i].z, fmaf(rest, s[i].z, k[i] * v[2]));
+    s[i].w = fmaf(g, s[i].w, fmaf(rest, s[i].w, k[i] * v[3]));
     o.x = fmaf(q[i], s[i].x, o.x); o.y = fmaf(q[i], s[i].y, o.y);
     o.z = fmaf(q[i], s[i].z, o.z); o.w = fmaf(q[i], s[i].w, o.w);
     S[i * kStep] = s[i];
