@@ -37,3 +37,37 @@ def test_decode_over_thousands_of_steps():
     for h in range(H):
         off = (S[:, h].cpu().double() - want[:, h]).norm() / want[:, h].norm()
         assert off <= steps ** 0.5 * 2.0 ** -24, (h, float(off * 2 ** 24))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("chunks,enters", [(7, 0), (8, 7), (8, 6), (15, 13), (16, 0)])
+def test_forward_over_a_few_chunks(chunks, enters, dt):
+    """One contribution alone: the first state (enters = 0), or the last token of chunk `enters` - 1, whose own factor is
+    1; it decays over the chunks after it. The mean of the relative errors over all elements, where the n + 1 roundings of
+    at most 2^-24 are worth 4 sqrt((n + 1) / elements) of that (their spread is at most 1 / sqrt(3) of it)."""
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    B, H, Dk, Dv = 64, 4, 32, 16
+    C = 64 if dt == BF16 else 32
+    T = chunks * C
+    assert gdn.gdn2_linattn_workspace_bytes(0, B, T, H, H, Dk, Dv, dt) == 0  # whole sequences
+    ld = badly_rounded(np.log(0.1) / C, np.log(0.9) / C, H, C)
+    g = torch.Generator().manual_seed(chunks + enters)
+    q, k = torch.zeros(B, T, H, Dk), torch.zeros(B, T, H, Dk)
+    v = torch.zeros(B, T, H, Dv)
+    S0 = None
+    if enters == 0:
+        S0 = torch.randn(B, H, Dk, Dv, generator=g)
+        want, n = S0.double(), chunks
+    else:
+        at = enters * C - 1
+        k[:, at] = torch.randn(B, H, Dk, generator=g).to(dt).float()
+        v[:, at] = torch.randn(B, H, Dv, generator=g).to(dt).float()
+        want, n = k[:, at].double()[..., :, None] * v[:, at].double()[..., None, :], chunks - enters
+    want = torch.exp(ld.double() * n * C)[None, :, None, None] * want
+    _, S = gdn.gdn2_linattn_fwd_chunked(*(t.to(dt).cuda() for t in (q, k, v)), ld.cuda(),
+                                        S0=None if S0 is None else S0.cuda())
+    for h in range(H):
+        rel = (S[:, h].cpu().double() / want[:, h] - 1).flatten()
+        assert abs(rel.mean()) <= 4 * ((n + 1) / rel.numel()) ** 0.5 * 2.0 ** -24, (h, float(rel.mean() * 2 ** 24))
+        assert rel.abs().max() <= (n + 1) * 2.0 ** -24, (h, float(rel.abs().max() * 2 ** 24))
