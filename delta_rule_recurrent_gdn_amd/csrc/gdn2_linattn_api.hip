@@ -207,7 +207,8 @@ int norm_sizes(int64_t tokens, int64_t period, int Hq, int Hk, int D, int rot, f
   if (tokens < 0 || Hq < 1 || Hk < 0 || D < 0 || rot < 0 || rot > D) return GDN2_ERR_SHAPE;
   if (tokens > 0 && period < 1) return GDN2_ERR_SHAPE;
   if (!(eps >= 0.f)) return GDN2_ERR_SHAPE;
-  if ((int64_t)Hq + Hk > (1 << 20) || tokens >= ((int64_t)1 << 26)) return GDN2_ERR_SHAPE;  // as above
+  // the grid as above: 256 threads for every four tokens, fewer than 2^32 in all
+  if ((int64_t)Hq + Hk > (1 << 20) || tokens > ((int64_t)1 << 26) - 4) return GDN2_ERR_SHAPE;
   if (!dim_ok(D) || rot % 16 != 0) return GDN2_ERR_UNSUPPORTED;
   if ((flags & ~(GDN2_FLAG_L2_NORM | GDN2_FLAG_INTERLEAVED)) != 0) return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;

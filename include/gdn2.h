@@ -386,8 +386,9 @@ int gdn2_fwd_chunked_noalloc(const void* q, const void* k, const void* v, const 
  *   cu_seqlens and states [N,H,Dk,Dv] as in gdn2_fwd_varlen, tokens outside every sequence left unwritten.
  * - H is a multiple of Hk: head h of v and of the states shares the q and k of head h / (H / Hk); dq and dk are
  *   the sums over the heads that share them (fp32, in a fixed order).
- * - Dk, Dv in {16, 32, 64, 128}; T >= 0 of any length (T = 0 writes S_final = S0, dS0 = dS_final). The library
- *   chooses the tiling; it does not change the result beyond the order of fp32 sums.
+ * - Dk, Dv in {16, 32, 64, 128}; 0 <= T <= 2^30 (T = 0 writes S_final = S0, dS0 = dS_final); fewer than 2^20 states
+ *   (sequences times H), of decode 2^24: more is GDN2_ERR_SHAPE. The library chooses the tiling; it does not change
+ *   the result beyond the order of fp32 sums.
  * - log_decay <= 0 as a rule; -inf (g = 0) is exact. Growth (log_decay > 0) follows the formula until fp32
  *   overflows. The decay is a constant: no gradient with respect to log_decay is formed (a decay for each token
  *   and head, with its gradient, is gdn2_fwd_chunked_ex's GDN2_FLAG_SCALAR_DECAY).
@@ -444,6 +445,7 @@ int gdn2_linattn_decode_step_slots(const void* q, const void* k, const void* v, 
  *   fused projection's rows; k likewise (k may be NULL with Hk = 0). q_out, k_out: rows q_out_stride, k_out_stride
  *   apart (Hq D for the contiguous q that the mixers take); q_out may be q with the same stride. Type dt throughout,
  *   strides multiples of 16 bytes and at least a row. D in {16, 32, 64, 128}; rot a multiple of 16, 0 <= rot <= D.
+ *   At most 2^26 - 4 tokens, Hq + Hk <= 2^20 (GDN2_ERR_SHAPE).
  * - q_weight, k_weight [D] fp32, nullable (ones); inv_freq [rot/2] fp32.
  * - positions int64: row n has positions[n % period] (period = T for positions shared by a batch's rows, else
  *   tokens); NULL: n % period. Any int64 value; the angle is formed and reduced in fp64 (off by at most its size

@@ -140,3 +140,16 @@ def test_rows_of_a_projection():
     for bad in (q[:, :2], q.transpose(0, 1), q[..., :2], q[:, :, ::2], q.transpose(2, 3)):
         with pytest.raises(ValueError, match="side by side|evenly spaced"):
             _rows("q", bad)
+
+
+@pytest.mark.parametrize("heads", [(1, 0), (16, 16)])
+@pytest.mark.parametrize("D", [16, 128])
+def test_norm_token_limit(heads, D):
+    """Four tokens a workgroup of 256 threads, a grid of fewer than 2^32: 2^26 - 4 tokens are the most."""
+    last = (1 << 26) - 4
+    bytes_of = _lib.load().gdn2_qk_norm_rope_workspace_bytes
+    assert bytes_of(last, *heads, D) > 0
+    for n in (last + 1, last + 2, last + 3, last + 4):
+        assert bytes_of(n, *heads, D) == 0
+        assert norm(n=n, D=D, Hq=heads[0], Hk=heads[1], rot=16, sq=4096, sk=4096, so=4096, sko=4096) == SHAPE
+        assert norm_bwd(n=n) == SHAPE
