@@ -88,16 +88,36 @@ def decode_bytes(B, H, d, e_in=2):
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "gdn2_fwd_bwd_B8H16T4096_hbm_traffic.md")
 
 
+CSRC = os.path.join(ROOT, "delta_rule_recurrent_gdn_amd", "csrc")
+# what holds the kernels of the traffic profile: records, chains, gradient scale, gradients, single-pass forward
+PROFILED_SOURCES = ("gdn2_prep", "gdn2_chain", "gdn2_gscale", "gdn2_bwd", "gdn2_bwd_d16", "gdn2_bwd_d32", "gdn2_bwd_d64",
+                    "gdn2_bwd_d128", "gdn2_bwd_d128f", "gdn2_fwd")
+
+
+def kernel_sources():
+    """The HIP sources of the profiled kernels with the headers that they include, sorted by name. The other operators'
+    sources and the entry points are not among them."""
+    import re
+
+    todo, found = [n + ".hip" for n in PROFILED_SOURCES], set()
+    while todo:
+        n = todo.pop()
+        if n in found or not os.path.exists(os.path.join(CSRC, n)):
+            continue
+        found.add(n)
+        with open(os.path.join(CSRC, n)) as f:
+            todo += re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+    return sorted(found)
+
+
 def kernel_sources_sha256():
-    """sha256 over the HIP sources (name and bytes of every .hip / .h file, sorted by name)."""
+    """sha256 over the profiled kernels' sources (name and bytes of each)."""
     import hashlib
 
-    d = os.path.join(ROOT, "delta_rule_recurrent_gdn_amd", "csrc")
     h = hashlib.sha256()
-    for n in sorted(os.listdir(d)):
-        if n.endswith((".hip", ".h")):
-            with open(os.path.join(d, n), "rb") as f:
-                h.update(n.encode() + b"\0" + f.read())
+    for n in kernel_sources():
+        with open(os.path.join(CSRC, n), "rb") as f:
+            h.update(n.encode() + b"\0" + f.read())
     return h.hexdigest()
 
 

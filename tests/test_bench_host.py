@@ -40,3 +40,37 @@ def test_byte_and_flop_models_match_the_stated_per_token_figures():
     assert bench.bwd_bytes(64, 128) == 6144
     assert round(bench.fwd_flops(64, 128)) == 181589
     assert round(bench.bwd_flops(64, 128)) == 476501
+
+
+def test_traffic_outlives_changes_to_other_operators(tmp_path, monkeypatch):
+    """The counters were taken on the training step's kernels: a change to another operator's sources, or a new one, keeps
+    the figure; a change to a kernel of the step or to a header that it includes takes it away."""
+    import shutil
+
+    csrc = tmp_path / "csrc"
+    shutil.copytree(os.path.join(ROOT, "delta_rule_recurrent_gdn_amd", "csrc"), csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    monkeypatch.setattr(bench, "CSRC", str(csrc), raising=False)
+    (tmp_path / "delta_rule_recurrent_gdn_amd").mkdir()
+    (tmp_path / "delta_rule_recurrent_gdn_amd" / "csrc").symlink_to(csrc)
+    with open(bench.TRAFFIC_PROFILE) as f:
+        text = f.read()
+    prof = tmp_path / "traffic.md"
+    monkeypatch.setattr(bench, "TRAFFIC_PROFILE", str(prof))
+    prof.write_text(text.replace(text.split("sources_sha256: ")[1].split("\n")[0], bench.kernel_sources_sha256()))
+    key = "bwd_records_launch_traffic_bytes"
+    assert isinstance(bench.measured_traffic(key), int)
+    for other in ("gdn2_linattn_impl.h", "gdn2_qk_norm.hip", "gdn2_decode.hip", "gdn2_new_operator.hip"):
+        with open(csrc / other, "a") as f:
+            f.write("// another line\n")
+        assert isinstance(bench.measured_traffic(key), int), other
+    for own in ("gdn2_bwd_impl.h", "gdn2_common.h", "gdn2_chain.hip", "gdn2_bwd_d128.hip", "gdn2_gscale.hip"):
+        before = (csrc / own).read_text()
+        (csrc / own).write_text(before + "// another line\n")
+        assert bench.measured_traffic(key) is None, own
+        (csrc / own).write_text(before)
+    assert isinstance(bench.measured_traffic(key), int)
+
+
+def test_the_committed_counters_are_of_the_present_kernels():
+    assert isinstance(bench.measured_traffic("bwd_records_launch_traffic_bytes"), int)
