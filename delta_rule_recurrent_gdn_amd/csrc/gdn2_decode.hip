@@ -143,7 +143,9 @@ __global__ __launch_bounds__((DecodeShape<DK, DV>::kThreads)) void gdn2_decode_k
     const int c = rg + RG * row_of(i);
     const float kc = s_k[c];
     const float4 n = make_float4(s[i].x + kc * u.x, s[i].y + kc * u.y, s[i].z + kc * u.z, s[i].w + kc * u.w);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, n), Sr, voff, row_of(i) * kRowStep, 0);
+    // the row offset in the vector one: a 16-byte store with a scalar offset, followed at once by a vector instruction
+    // that overwrites its data register, stores the new value in some lanes (no wait is put between the two)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, n), Sr, voff + row_of(i) * kRowStep, 0, 0);
   }
 }
 
