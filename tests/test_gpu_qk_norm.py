@@ -195,3 +195,33 @@ def test_refusals():
     for error, call in bad:
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("l2", [False, True], ids=["rms", "l2"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_fp32_gradients_of_bf16_inputs_row_by_row(case, l2, interleaved):
+    """As the main test, with gradients in fp32: dq, dk and both weights' gradients (weights with the L2 norm too)."""
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    lead, Hq, Hk, D, rot = case
+    x = make(D + rot + Hq + 1, lead, Hq, Hk, D, rot, BF16)
+    g = torch.Generator().manual_seed(rot + D)
+    dy = {"q": torch.randn(*lead, Hq, D, generator=g), "k": torch.randn(*lead, Hk, D, generator=g)}
+    d = {n: t.cuda() for n, t in x.items()}
+    kw = dict(eps=1e-3, l2=l2, interleaved=interleaved)
+    q, k = cut(x, Hq, Hk, D)
+    gq, gk = cut(d, Hq, Hk, D)
+    got = gdn.gdn2_qk_norm_rope_bwd(dy["q"].cuda(), dy["k"].cuda(), gq, gk, d["pos"], d["f"].float() if rot else None,
+                                    q_weight=d["wq"], k_weight=d["wk"], q_scale=0.25, **kw)
+    for n, t, w, s in (("q", q, x["wq"], 0.25), ("k", k, x["wk"], 1.0)):
+        dx, dw = O.qk_norm_rope_backward(dy[n], t, x["pos"].numpy(), x["f"].float(), w, scale=s, **kw)
+        t64, dy64 = np.abs(t.double().numpy()), np.abs(dy[n].double().numpy())
+        m = (t64 ** 2).sum(-1, keepdims=True) / (1 if l2 else D) + 1e-3
+        h = s * 2 * dy64.max(-1, keepdims=True) * np.abs(w.numpy())
+        mag = h / np.sqrt(m) + t64 * (h * t64).sum(-1, keepdims=True) / ((1 if l2 else D) * m ** 1.5)
+        assert got["d" + n].dtype == BF16
+        near("d" + n, got["d" + n], dx, mag, D)
+        rows = t64.reshape(-1, D).shape[0]
+        terms = (s * 2 * dy64.max(-1, keepdims=True) * t64 / np.sqrt(m)).reshape(-1, D).sum(0)
+        assert (np.abs(got[f"d{n}_weight"].cpu().double().numpy() - dw) <= (rows + D + 64) * 2.0 ** -24 * terms).all(), n
