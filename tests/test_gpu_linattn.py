@@ -442,3 +442,21 @@ def test_states_and_rows_past_32_bits():
     assert (o[0, :100] == 0).all() and (o[-2, -100:] == 0).all()
     torch.testing.assert_close(S[-1:], S1, rtol=0, atol=1e-5 * float(S1.abs().max()))
     torch.testing.assert_close(o[-1:, -1000:].float(), o1[:, -1000:].float(), rtol=2 ** -7, atol=1e-2)
+
+
+@pytest.mark.parametrize("T", [900, 1025])
+def test_pieces_at_the_largest_heads(T):
+    """bf16 at 128 x 128, cut into pieces: forward, backward and states against the oracle."""
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    x = make(50 + T, 1, T, 1, 2, 128, 128, BF16, decay=-4e-3)
+    d = dev(x)
+    assert gdn.gdn2_linattn_workspace_bytes(0, 1, T, 1, 2, 128, 128, BF16) > 0
+    (o, S), (mo, mS) = oracle_fwd(x, scale=0.1)
+    go, gS = gdn.gdn2_linattn_fwd_chunked(d["q"], d["k"], d["v"], d["ld"], S0=d["S0"], scale=0.1)
+    check("o", go, o, mo, T, 128)
+    check("S", gS, S, mS, T, 128)
+    g, m = oracle_bwd(x, scale=0.1)
+    got = gdn.gdn2_linattn_bwd_chunked(d["q"], d["k"], d["v"], d["ld"], d["dO"], S0=d["S0"], dS_final=d["dS"], scale=0.1)
+    for n in g:
+        check(n, got[n], g[n], m[n], T, 128)
