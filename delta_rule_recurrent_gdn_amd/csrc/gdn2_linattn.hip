@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kJoinThreads) void gdn2_linattn_join_kernel(LinArgs
   if (!a.pieces) return;
   const float ld = a.log_decay[h];
   const double d = exp((ld < -1e4f ? -1e4 : (double)ld) * a.seg_tok);
-  const float hi = (float)d, lo = (float)(d - hi);
+  const float hi = (float)d, lo = hi <= 3.4028235e38f ? (float)(d - hi) : 0.f;
   float4* p = reinterpret_cast<float4*>(sw.seg_state + ((int64_t)slot * a.H + h) * state + at);
   const int64_t stride = (int64_t)step * a.H * state / 4;
   p[0] = make_float4(z[0], z[1], z[2], z[3]);
@@ -63,7 +63,8 @@ __global__ __launch_bounds__(kJoinThreads) void gdn2_linattn_join_kernel(LinArgs
     if (s + 1 < nseg) next = p[(s + 1) * stride];
     const float add[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = fmaf(z[e], hi, fmaf(z[e], lo, add[e]));
+    for (int e = 0; e < 4; ++e)  // a state of zeros stays as it is, also where growth over a piece is no fp32 number
+      z[e] = z[e] == 0.f ? add[e] : fmaf(z[e], hi, fmaf(z[e], lo, add[e]));
     p[s * stride] = make_float4(z[0], z[1], z[2], z[3]);
   }
 }

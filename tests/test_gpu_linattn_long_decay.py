@@ -71,3 +71,34 @@ def test_forward_over_a_few_chunks(chunks, enters, dt):
         rel = (S[:, h].cpu().double() / want[:, h] - 1).flatten()
         assert abs(rel.mean()) <= 4 * ((n + 1) / rel.numel()) ** 0.5 * 2.0 ** -24, (h, float(rel.mean() * 2 ** 24))
         assert rel.abs().max() <= (n + 1) * 2.0 ** -24, (h, float(rel.abs().max() * 2 ** 24))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "fp32"])
+def test_growth_after_padding(dt):
+    """log_decay = 0.4 over 1500 tokens, of which all but the last 50 are zeros: nothing grows past e^20, though the
+    growth over one of the pieces that the sequence is cut into is no fp32 number."""
+    import delta_rule_recurrent_gdn_amd as gdn
+
+    import oracle.linattn as O
+
+    T, D = 1500, 32
+    assert gdn.gdn2_linattn_workspace_bytes(0, 1, T, 1, 1, D, D, dt) > 0
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(1, T, 1, D, generator=g).to(dt) for _ in range(3))
+    k[:, :T - 50] = 0
+    ld = torch.tensor([0.4])
+    (o, S), (mo, mS) = (O.linattn_forward(f(q), f(k), f(v), ld) for f in (lambda t: t, torch.abs))
+    got, last = gdn.gdn2_linattn_fwd_chunked(q.cuda(), k.cuda(), v.cuda(), ld.cuda())
+    for name, x, ref, mag in (("o", got, o, mo), ("S", last, S, mS)):
+        x = x.cpu().double().numpy()
+        tol = (2.0 ** -8 if name == "o" and dt == BF16 else 0) * np.abs(ref) + (4 * (50 + D) + 64) * 2.0 ** -24 * mag
+        assert np.isfinite(x).all() and (np.abs(x - ref) <= tol).all(), name
+    # the reversed recurrences: zeros at the end of dO
+    dO = torch.randn(1, T, 1, D, generator=g).to(dt)
+    dO[:, 50:] = 0
+    want, mag = (O.linattn_backward(f(q), f(k), f(v), ld, f(dO)) for f in (lambda t: t, torch.abs))
+    r = gdn.gdn2_linattn_bwd_chunked(q.cuda(), k.cuda(), v.cuda(), ld.cuda(), dO.cuda())
+    for n in ("dk", "dv", "dS0"):
+        x = r[n].cpu().double().numpy()
+        tol = (2.0 ** -8 if n != "dS0" and dt == BF16 else 0) * np.abs(want[n]) + (4 * (50 + D) + 64) * 2.0 ** -24 * mag[n]
+        assert np.isfinite(x).all() and (np.abs(x - want[n]) <= tol).all(), n
