@@ -17,7 +17,7 @@ struct LinSweep {
   const void* x;
   const void* y;
   const void* z;
-  void* r;                       // [rows, H / rdiv, E] of the inputs' type, or fp32 [rows, H, E] when r_f32
+  void* r;                       // [rows, H, E] of the inputs' type, or fp32 when r_f32
   int xdiv, ydiv, zdiv;          // head h reads head h / div of the tensor
   bool r_f32;
   bool rev;                      // walk every sequence from its last token to its first

@@ -163,11 +163,14 @@ __global__ __launch_bounds__(256) void gdn2_linattn_group_sum_kernel(const float
 
 }  // namespace
 
-// Tokens a piece: as many pieces as give every CU its one workgroup (the sweeps' LDS holds one; twice as many, in two
-// rounds: 64K tokens of 16 heads, forward, 443 -> 465 us, 2 x 2055 tokens, backward, 79 -> 102), of at least four
+// Tokens a piece: about as many pieces as give every CU its one workgroup (the sweeps' LDS holds one; twice as many, in
+// two rounds: 64K tokens of 16 heads, forward, 443 -> 465 us, 2 x 2055 tokens, backward, 79 -> 102), of at least four
 // chunks (fewer cost more in states written, joined and read than the shorter walk saves: 2 x 2055 tokens of 12
 // heads, backward, 115 us with four chunks a piece, 137 with two, 118 with eight; fp32, 2 x 1001 of 8 heads, whose
-// chunks are half as long: 27 us with four, 36 with eight, 56 with sixteen).
+// chunks are half as long: 27 us with four, 36 with eight, 56 with sixteen). It is no exact round: past 128 heads and
+// column groups of all sequences there is one piece each; a backward of equal head sizes is counted with two sweeps
+// and runs three; a packed batch is cut as one row of tokens, and every sequence's last piece comes on top (11 prompts
+// of 14029 tokens: 336 to 368 workgroups by their lengths).
 int linattn_seg_tokens(int N, int T, int H, int E, int sweeps, bool packed, bool f32) {
   constexpr int kUnit = 64, kWorkgroups = 256;
   const int64_t units = (T + kUnit - 1) / kUnit, least = f32 ? 2 : 4;

@@ -4,7 +4,7 @@
 //
 // HBM-bound: 8 Dk Dv bytes of state an entry and head, five operations an element. One workgroup per (entry, head);
 // a thread owns 4 neighbouring value columns of RPT key rows, so every access of a wave is one contiguous block.
-// 256 entries of 16 heads, d 128 (0.54 GB): 108 us, 5.0 TB/s, with the states out of the caches; one entry: 4 us.
+// 256 entries of 16 heads, d 128 (0.54 GB): 109 us, 4.9 TB/s, with the states out of the caches; one entry: 4 us.
 // The new state goes out as soon as it is formed; only the column sums of o meet in LDS. It goes through plain
 // pointers: a 16-byte buffer store with a scalar offset, followed at once by a vector instruction that overwrites its
 // data register, stored the new value in some lanes (no wait is put between the two for that form of store).

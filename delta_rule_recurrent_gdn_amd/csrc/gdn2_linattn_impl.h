@@ -19,13 +19,15 @@
 // that x is read in from LDS with one 16-byte access, so the state enters its product from the registers it is
 // kept in. The contraction over tokens reads y and z column-wise with the transposing LDS read (16 bit).
 //
-// What bounds it (B8 H16 T4096 d128 bf16, 256 workgroups, one a CU): 159-165 us by card, 3.4 TB/s of the 0.54 GB that
-// it has to read and write, once each by the counters (a copy: 5.2 TB/s, 105 us). The loads alone take 98 us, the
-// state's waves with their data at hand 126: with one workgroup a CU and a barrier a chunk the two cover each other in
-// part. Of the SIMDs' time vector instructions take 39 %, the matrix cores 27 %; LDS is busy for 32 %, and its
-// conflicts are not what is waited for. So the work is split by role: the state's waves never wait for memory (249 us
-// with one role, 161 with loading waves that also form the scores). 64K tokens of one sequence: 442-468 us, 2.4 TB/s
-// of 1.07 GB: y and z are read a second time, for the pieces' states.
+// What bounds it (B8 H16 T4096 d128 bf16, 256 workgroups, one a CU): 180 us, 3.0 TB/s of the 0.54 GB that it has to read
+// and write, once each by the counters (a copy: 5.2 TB/s, 105 us). Nothing is full: of the SIMDs' time vector
+// instructions take 44 %, the matrix cores 29 %; LDS is busy for 32 %, a quarter of that in conflicts. The waves wait
+// for 39 % of their time (5 % for LDS instructions) and for 20 % to issue. With two bf16 terms for scores and states the
+// loads alone took 98 us, the state's waves with their data at hand 126, together 157: with one workgroup a CU, one wave
+// of the state a SIMD and a barrier a chunk the two cover each other in part. So the work is split by role: the state's
+// waves never wait for memory (two terms: 249 us with one role, 161 with loading waves that also form the scores). 64K
+// tokens of one sequence: 490-499 us, 2.2 TB/s of 1.07 GB: y and z are read a second time, for the pieces' states.
+// Comparisons of 160 to 167 us below were measured with two terms.
 //
 // Precision (16-bit inputs): products of two inputs are exact in the matrix cores' fp32 sums. The scores, the decayed
 // z and the state as an operand are split into three bf16 terms each, which hold an fp32 value's 24 bits: r and the

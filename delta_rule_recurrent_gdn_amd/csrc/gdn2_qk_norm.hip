@@ -7,8 +7,9 @@
 //
 // HBM-bound: x in, y out (backward: x and dy in, dx out), about 15 operations an element. A wave takes a token, or a
 // share of its heads where there are few tokens; D / 8 lanes own a head's row, 8 channels (16 bytes of bf16) a lane.
-// 32768 tokens of 16 + 16 heads, D 128, bf16: forward 101 us (5.3 TB/s of 0.54 GB, a copy's rate), backward 181 us (4.4
-// of 0.81 GB: three streams, and the vector work beside them; 215 with its rows converted as they arrive).
+// 32768 tokens of 16 + 16 heads, D 128, bf16: forward 101 us (5.3 TB/s of 0.54 GB, a copy's rate), backward 181 us: 160
+// for the rows (5.0 of 0.81 GB; 215 in all with its rows converted as they arrive) and 21 for the sums of the weights'
+// gradients, 16 workgroups that each add 64 values a thread one after another.
 // A token's angles are the same for all its heads, so lane j forms the cosine and sine of pair j once (the angle in
 // turns in fp64, reduced, then fp32) and the rows read them from LDS.
 
