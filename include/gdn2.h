@@ -390,8 +390,9 @@ int gdn2_fwd_chunked_noalloc(const void* q, const void* k, const void* v, const 
  *   (sequences times H), of decode 2^24: more is GDN2_ERR_SHAPE. The library chooses the tiling; it does not change
  *   the result beyond the order of fp32 sums.
  * - log_decay <= 0 as a rule; -inf (g = 0) is exact. Growth (0 < log_decay <= 1.3: the powers of g over 64 tokens
- *   are formed in fp32) follows the formula until fp32 overflows. The decay is a constant: no gradient with respect to log_decay is formed (a decay for each token
- *   and head, with its gradient, is gdn2_fwd_chunked_ex's GDN2_FLAG_SCALAR_DECAY).
+ *   are formed in fp32) follows the formula until fp32 overflows. The decay is a constant: no gradient with respect to
+ *   log_decay is formed (a decay for each token and head, with its gradient, is gdn2_fwd_chunked_ex's
+ *   GDN2_FLAG_SCALAR_DECAY).
  * - An infinity or NaN in a token never reaches an earlier token's output (of gradients: dq's; a later token's dk
  *   and dv), nor another sequence's; the state it enters is not finite from there on.
  * - Deterministic, asynchronous on `stream`, no allocation; the general conventions above. Scores, states and sums
